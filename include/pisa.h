@@ -312,6 +312,121 @@ pisa_status pisa_get_tuning(int batch, int heads, int L, int d, int block, pisa_
 pisa_status pisa_tuning_save(const char* path);
 pisa_status pisa_tuning_load(const char* path);
 
+/* Element strides of a [batch, heads, rows, d] tensor whose last dimension is
+ * contiguous.  A stride of a dimension of size 1 is not read. */
+typedef struct pisa_strides {
+  int64_t batch, head, row;
+} pisa_strides;
+
+/* ---- Rotary positions of the queries and keys --------------------------
+ * A diffusion transformer turns q and k by their tokens' positions before the
+ * self-attention above.  Pair p of a head holds (u, w) and belongs to one axis
+ * of the token grid; with angle = position[token][axis_p] * freq_p and
+ * magnitude m:
+ *     u' = m (u cos angle - w sin angle),  w' = m (u sin angle + w cos angle).
+ * Layouts: interleaved, pair p = elements (2p, 2p + 1); half, pair p =
+ * elements (p, p + P) with P pairs in all.  Elements from 2P on are copied.
+ *
+ * Axis a of even size D_a (elements) owns D_a / 2 consecutive pairs, with
+ * freq_i = theta^(-2 i / D_a), i = 0 .. D_a / 2 - 1, and m = 1.  Scaling for
+ * contexts `factor` times longer than the trained one:
+ *   LINEAR  freq_i / factor (position interpolation)
+ *   NTK     theta replaced by theta factor^(D_a / (D_a - 2))  (D_a > 2): the
+ *           slowest pair is slowed by `factor`, the fastest not at all
+ *   YARN    g freq_i + (1 - g) freq_i / factor, with g = clamp((r_i - 1) / 31,
+ *           0, 1) and r_i = original_len freq_i / (2 pi) the turns that the
+ *           pair makes in the trained context; m = 0.1 ln(factor) + 1. */
+#define PISA_ROPE_MAX_PAIRS 64
+#define PISA_ROPE_MAX_AXES 3
+
+typedef enum pisa_rope_layout {
+  PISA_ROPE_INTERLEAVED = 0,
+  PISA_ROPE_HALF = 1
+} pisa_rope_layout;
+
+typedef enum pisa_rope_scaling {
+  PISA_ROPE_SCALE_NONE = 0,
+  PISA_ROPE_SCALE_LINEAR = 1,
+  PISA_ROPE_SCALE_NTK = 2,
+  PISA_ROPE_SCALE_YARN = 3
+} pisa_rope_scaling;
+
+/* What pisa_rope needs to know of its positions: filled by
+ * pisa_rope_make_plan, or by the caller for other frequencies. */
+typedef struct pisa_rope_plan {
+  int layout;                               /* pisa_rope_layout            */
+  int axes;                                 /* 1 .. PISA_ROPE_MAX_AXES     */
+  int pairs;                                /* 1 .. PISA_ROPE_MAX_PAIRS    */
+  float magnitude;                          /* finite                      */
+  double freq[PISA_ROPE_MAX_PAIRS];         /* finite                      */
+  unsigned char axis[PISA_ROPE_MAX_PAIRS];  /* < axes                      */
+} pisa_rope_plan;
+
+/* Fills `plan` (host arithmetic, no CUDA call).  axis_dim[a]: even, at least
+ * 2, together at most 2 PISA_ROPE_MAX_PAIRS.  theta > 0; factor >= 1 and (YARN)
+ * original_len >= 1 are read where the scaling uses them. */
+pisa_status pisa_rope_make_plan(int axes, const int* axis_dim, double theta, pisa_rope_layout layout,
+                                pisa_rope_scaling scaling, double factor, int original_len,
+                                pisa_rope_plan* plan);
+
+/* Turns q [batch, heads, L, d] and, when k is not NULL, k [batch, kv_heads, L,
+ * d] in one launch.  strides: those of {q, q_out, k, k_out}, or NULL when all
+ * are dense; the output may have other strides than the input (so a projection
+ * [batch, L, heads, d] becomes the [batch, heads, L, d] that the attention
+ * reads), and may be the input itself with the same strides (in place); no
+ * other overlap is allowed.  Pointers need only the element's alignment; where
+ * pointers and strides are multiples of 16 bytes and the number of pairs is
+ * one of the vector width (4 bf16 / 2 fp32 interleaved, 8 / 4 half), accesses
+ * are 16 bytes wide.  positions: float32 [L, axes] shared by the batch
+ * (positions_batch_stride = 0), or one such table per batch entry at that
+ * distance in elements.  backward != 0: q and k are output gradients, the
+ * result is the input gradients (the transposed map).  Angles are formed in 64
+ * bits, the rotation in 32; one rounding to the element type.
+ * d in {64, 128}, 2 plan->pairs <= d. */
+pisa_status pisa_rope(const void* q, void* q_out, const void* k, void* k_out, pisa_dtype dtype, int batch,
+                      int heads, int kv_heads, int L, int d, const pisa_strides* strides,
+                      const float* positions, int64_t positions_batch_stride, const pisa_rope_plan* plan,
+                      int backward, void* stream);
+
+/* ---- Cross-attention to an encoder's states -----------------------------
+ * q, out [batch, heads, Lq, d]; k, v [batch, kv_heads, Lk, d] with heads a
+ * multiple of kv_heads: query head h reads key head h / (heads / kv_heads).
+ *     out_i = sum_j p_ij v_j,  p_i = softmax over the allowed keys of q_i . k_j / sqrt(d)
+ *     lse_i = ln sum_j exp(q_i . k_j / sqrt(d))                   (float32 [batch, heads, Lq])
+ * Key j of batch entry b is allowed when j < kv_len[b] (kv_len NULL: every j;
+ * values are clamped to [0, Lk]) and key_mask[b][j] != 0 (key_mask NULL: every
+ * j).  Keys and values that are not allowed take part in no product, whatever
+ * their memory holds.  Without any allowed key out = 0, lse = -inf, and the
+ * gradients are zero.
+ *
+ * strides: those of {q, k, v, out} (forward) or {dout, q, k, v, out, dq, dk,
+ * dv} (backward), or NULL when all are dense.  Every stride of a dimension
+ * larger than 1 is a multiple of 16 bytes and at least d (so no broadcast
+ * tensors); pointers are 16-byte aligned, kv_len and lse 4-byte, key_mask any.
+ * d in {64, 128}, batch * heads <= 65535.  Softmax statistics and sums are
+ * 32-bit; with bf16 inputs p and ds enter their products rounded to bf16. */
+
+/* Scratch bytes of pisa_cross_attn_fwd (backward = 0) or pisa_cross_attn_bwd
+ * (backward = 1); masked: whether kv_len or key_mask is given.  0 for an
+ * unsupported shape; a forward may need none, which is returned as 16. */
+size_t pisa_cross_workspace_size(pisa_dtype dtype, int batch, int heads, int kv_heads, int Lq, int Lk, int d,
+                                 int masked, int backward);
+
+/* Forward.  lse may be NULL. */
+pisa_status pisa_cross_attn_fwd(const void* q, const void* k, const void* v, void* out, float* lse,
+                                pisa_dtype dtype, int batch, int heads, int kv_heads, int Lq, int Lk, int d,
+                                const pisa_strides* strides, const int32_t* kv_len, const uint8_t* key_mask,
+                                void* workspace, size_t workspace_bytes, void* stream);
+
+/* Backward: dq, dk, dv from dout and the forward's out and lse (same mask).
+ * dk and dv are summed over the query heads that share a key head, in a fixed
+ * order (no float atomics: results are bit-reproducible). */
+pisa_status pisa_cross_attn_bwd(const void* dout, const void* q, const void* k, const void* v, const void* out,
+                                const float* lse, void* dq, void* dk, void* dv, pisa_dtype dtype, int batch,
+                                int heads, int kv_heads, int Lq, int Lk, int d, const pisa_strides* strides,
+                                const int32_t* kv_len, const uint8_t* key_mask, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
 /* Sets the limit of the bounded waits in the tensor-core kernels on the
  * current device, in nanoseconds of the GPU's global timer; 0 restores the
  * default of 2 s.  Every mbarrier wait between the warps of a CTA (operand

@@ -10,12 +10,16 @@ block_stats, cov_norm, cov_norm_spectral, block_first_order, select, select_rout
 attn_fwd_with_sel, attn_fwd_blockwise_with_sel, attn_fwd,
 attn_fwd_host, attn_fwd_with_sel_noalloc, keep_count, workspace_size, stats_workspace_size,
 fused_workspace_size, host_workspace_size, autotune, set_tuning, clear_tuning, get_tuning,
-tuning_save, tuning_load, set_wait_limit, device_status, status_string.
+tuning_save, tuning_load, set_wait_limit, device_status, status_string; and for
+the rest of a transformer block's attention, on tensors of any strides with a
+contiguous last dimension: rope, rope_bwd, cross_attn_fwd, cross_attn_bwd,
+cross_workspace_size.
 """
 
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional, Tuple
 
@@ -42,6 +46,8 @@ PISA_BF16 = 0
 PISA_FP32 = 1
 PISA_ROUTE_COVARIANCE = 0
 PISA_ROUTE_POOLED = 1
+ROPE_LAYOUTS = {"interleaved": 0, "half": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024  # PISA_NOALLOC_SCRATCH_BYTES
 
 EXPORTS = (
@@ -52,6 +58,7 @@ EXPORTS = (
     "pisa_attn_fwd_host", "pisa_select_route", "pisa_cov_norm_spectral", "pisa_autotune",
     "pisa_set_tuning", "pisa_get_tuning", "pisa_tuning_save", "pisa_tuning_load",
     "pisa_set_wait_limit", "pisa_attn_fwd_blockwise_with_sel",
+    "pisa_rope_make_plan", "pisa_rope", "pisa_cross_workspace_size", "pisa_cross_attn_fwd", "pisa_cross_attn_bwd",
 )
 
 _p = ctypes.c_void_p
@@ -101,6 +108,26 @@ _lib_fwd_blockwise = _sig("pisa_attn_fwd_blockwise_with_sel", _i, _p, _p, _p, _p
                           _p, _p, _p, _p, _i, _p)
 _lib_set_wait_limit = _sig("pisa_set_wait_limit", _i, ctypes.c_uint64, _p)
 _lib_fwd_host = _sig("pisa_attn_fwd_host", _i, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _f, _i, _p, _z, _p)
+
+
+class _Strides(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("head", ctypes.c_int64), ("row", ctypes.c_int64)]
+
+
+class _RopePlan(ctypes.Structure):
+    _fields_ = [("layout", _i), ("axes", _i), ("pairs", _i), ("magnitude", _f),
+                ("freq", ctypes.c_double * 64), ("axis", ctypes.c_ubyte * 64)]
+
+
+_SP = ctypes.POINTER(_Strides)
+_lib_rope_plan = _sig("pisa_rope_make_plan", _i, _i, ctypes.POINTER(_i), ctypes.c_double, _i, _i, ctypes.c_double,
+                      _i, ctypes.POINTER(_RopePlan))
+_lib_rope = _sig("pisa_rope", _i, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _p, _p, ctypes.c_int64, _p, _i, _p)
+_lib_cross_ws = _sig("pisa_cross_workspace_size", _z, _i, _i, _i, _i, _i, _i, _i, _i, _i)
+_lib_cross_fwd = _sig("pisa_cross_attn_fwd", _i, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _p, _p, _p,
+                      _p, _z, _p)
+_lib_cross_bwd = _sig("pisa_cross_attn_bwd", _i, _p, _p, _p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i,
+                      _p, _p, _p, _p, _z, _p)
 
 
 class PisaError(RuntimeError):
@@ -369,6 +396,204 @@ def tuning_save(path: str):
 
 def tuning_load(path: str):
     _check(_lib_tuning_load(os.fsencode(path)), "pisa_tuning_load")
+
+
+class _LaunchOn:
+    """The stream and device that a call launches and allocates on: ``stream``,
+    or the current stream of the tensors' device.  Tensors made here for
+    another stream than the current one are kept from reuse until both are
+    done with them (keep())."""
+
+    def __init__(self, device: torch.device, stream: Optional[torch.cuda.Stream]):
+        self.current = torch.cuda.current_stream(device)
+        self.stream = self.current if stream is None else stream
+        if self.stream.device != device:
+            raise ValueError("stream is not on the tensors' device")
+        self.other = self.stream != self.current
+        self.ctx = (torch.cuda.stream(self.stream)
+                    if self.other or torch.cuda.current_device() != device.index else None)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return ctypes.c_void_p(self.stream.cuda_stream)
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+    def keep(self, *tensors):
+        if self.other:
+            for t in tensors:
+                t.record_stream(self.current)
+
+
+def _same_kind(first: torch.Tensor, *others: torch.Tensor) -> None:
+    for t in (first,) + others:
+        if not t.is_cuda or t.dim() != 4 or t.stride(3) != 1 and t.shape[3] != 1:
+            raise ValueError("tensors must be 4-d CUDA tensors with a contiguous last dimension")
+        if t.dtype != first.dtype or t.device != first.device:
+            raise ValueError("tensors must share one dtype and one device")
+
+
+def _strides(*ts: Optional[torch.Tensor]):
+    """pisa_strides of the tensors, or None when all are dense."""
+    if all(t is None or t.is_contiguous() for t in ts):
+        return None
+    return (_Strides * len(ts))(*[(0, 0, 0) if t is None else t.stride()[:3] for t in ts])
+
+
+@functools.lru_cache(maxsize=256)
+def _rope_plan(axis_dims: Tuple[int, ...], theta: float, layout: str, scaling: str, factor: float,
+               original_len: int) -> _RopePlan:
+    if layout not in ROPE_LAYOUTS or scaling not in ROPE_SCALINGS:
+        raise ValueError(f"layout is one of {list(ROPE_LAYOUTS)}, scaling one of {list(ROPE_SCALINGS)}")
+    plan = _RopePlan()
+    dims = (_i * max(1, len(axis_dims)))(*axis_dims)
+    _check(_lib_rope_plan(len(axis_dims), dims, theta, ROPE_LAYOUTS[layout], ROPE_SCALINGS[scaling], factor,
+                          original_len, ctypes.byref(plan)), "pisa_rope_make_plan")
+    return plan
+
+
+def _rope(q, k, positions, axis_dims, theta, layout, scaling, factor, original_len, q_out, k_out, stream, backward):
+    plan = _rope_plan(tuple(axis_dims), float(theta), layout, scaling, float(factor), int(original_len))
+    _same_kind(q, *(t for t in (k, q_out, k_out) if t is not None))
+    b, h, L, d = q.shape
+    code = _dtype_code(q)
+    if k is not None and (k.shape[0] != b or k.shape[2:] != q.shape[2:]):
+        raise ValueError("q and k must agree in batch, length and head size")
+    for x, y in ((q, q_out), (k, k_out)):
+        if y is not None and (x is None or y.shape != x.shape):
+            raise ValueError("an output has the shape of its input")
+    if (positions.dtype != torch.float32 or positions.device != q.device or not positions.is_contiguous()
+            or positions.shape not in ((L, plan.axes), (b, L, plan.axes))):
+        raise ValueError("positions must be contiguous float32 [L, axes] or [batch, L, axes] on the same device")
+    on = _LaunchOn(q.device, stream)
+    with on as st:
+        made = []
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            made.append(q_out)
+        if k is not None and k_out is None:
+            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+            made.append(k_out)
+        _check(_lib_rope(_ptr(q), _ptr(q_out), _ptr(k), _ptr(k_out), code, b, h,
+                         0 if k is None else k.shape[1], L, d, _strides(q, q_out, k, k_out), _ptr(positions),
+                         L * plan.axes if positions.dim() == 3 else 0, ctypes.byref(plan), backward, st), "pisa_rope")
+    on.keep(*made)
+    return q_out, k_out
+
+
+def rope(q, k, positions, axis_dims, theta=10000.0, layout="interleaved", scaling="none", factor=1.0, original_len=0,
+         q_out=None, k_out=None, stream=None):
+    """Rotary positions: (q_out, k_out) for q [b,h,L,d] and k [b,hk,L,d] (or
+    None), of any strides with a contiguous last dimension.
+
+    ``positions``: float32 [L, axes] or [b, L, axes].  ``axis_dims``: the head
+    elements that each axis turns (even; what is left of the head is copied),
+    with frequencies ``theta ** (-2 i / dim)``.  ``layout``: pairs of
+    "interleaved" neighbours, or the first "half" with the second.  ``scaling``
+    for contexts ``factor`` times longer than trained: "linear" (positions
+    interpolated), "ntk" (larger theta), "yarn" (by parts; ``original_len`` is
+    the trained length).  Outputs are dense [b,h,L,d], as attn_fwd reads them,
+    unless given; an output may be its own input (in place)."""
+    return _rope(q, k, positions, axis_dims, theta, layout, scaling, factor, original_len, q_out, k_out, stream, 0)
+
+
+def rope_bwd(dq, dk, positions, axis_dims, theta=10000.0, layout="interleaved", scaling="none", factor=1.0,
+             original_len=0, q_out=None, k_out=None, stream=None):
+    """Gradients of rope's inputs from those of its outputs (same arguments)."""
+    return _rope(dq, dk, positions, axis_dims, theta, layout, scaling, factor, original_len, q_out, k_out, stream, 1)
+
+
+def cross_workspace_size(dtype: torch.dtype, batch, heads, kv_heads, Lq, Lk, d, masked=False, backward=False) -> int:
+    code = PISA_BF16 if dtype == torch.bfloat16 else PISA_FP32 if dtype == torch.float32 else -1
+    return int(_lib_cross_ws(code, batch, heads, kv_heads, Lq, Lk, d, 1 if masked else 0, 1 if backward else 0))
+
+
+def _cross_shapes(q, k, v, kv_len, key_mask):
+    b, h, Lq, d = q.shape
+    hk, Lk = k.shape[1], k.shape[2]
+    if k.shape != (b, hk, Lk, d) or v.shape != k.shape:
+        raise ValueError("q is [b,h,Lq,d], k and v are [b,hk,Lk,d]")
+    if kv_len is not None and (kv_len.dtype != torch.int32 or kv_len.shape != (b,) or not kv_len.is_contiguous()
+                               or kv_len.device != q.device):
+        raise ValueError("kv_len must be contiguous int32 [b] on the same device")
+    if key_mask is not None and (key_mask.dtype not in (torch.bool, torch.uint8) or key_mask.shape != (b, Lk)
+                                 or not key_mask.is_contiguous() or key_mask.device != q.device):
+        raise ValueError("key_mask must be contiguous bool or uint8 [b, Lk] on the same device")
+    return b, h, hk, Lq, Lk, d
+
+
+def _like(t: torch.Tensor) -> torch.Tensor:
+    """An empty tensor of t's shape with its dimensions in t's memory order."""
+    return torch.empty_like(t, memory_format=torch.preserve_format)
+
+
+def cross_attn_fwd(q, k, v, kv_len=None, key_mask=None, return_lse=False, out=None, workspace=None, stream=None):
+    """Attention of q [b,h,Lq,d] to an encoder's k, v [b,hk,Lk,d] (heads a
+    multiple of hk), softmax scale 1/sqrt(d).
+
+    ``kv_len`` int32 [b] and ``key_mask`` bool [b, Lk] (nonzero: allowed) say
+    which keys count; the others are not read into any product.  A row without
+    keys gives 0.  With ``return_lse``: (out, lse), lse float32 [b,h,Lq], as
+    cross_attn_bwd needs it.  Any strides with a contiguous last dimension that
+    are multiples of 16 bytes."""
+    _same_kind(q, k, v, *(() if out is None else (out,)))
+    code = _dtype_code(q)
+    b, h, hk, Lq, Lk, d = _cross_shapes(q, k, v, kv_len, key_mask)
+    if out is not None and out.shape != q.shape:
+        raise ValueError("out has the shape of q")
+    masked = 0 if kv_len is None and key_mask is None else 1
+    on = _LaunchOn(q.device, stream)
+    with on as st:
+        made = []
+        if out is None:
+            out = _like(q)
+            made.append(out)
+        lse = torch.empty(b, h, Lq, dtype=torch.float32, device=q.device) if return_lse else None
+        if return_lse:
+            made.append(lse)
+        ws = _workspace(_lib_cross_ws(code, b, h, hk, Lq, Lk, d, masked, 0), q.device, workspace)
+        _check(_lib_cross_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), code, b, h, hk, Lq, Lk, d,
+                              _strides(q, k, v, out), _ptr(kv_len), _ptr(key_mask), _ptr(ws), ws.numel(), st),
+               "pisa_cross_attn_fwd")
+    on.keep(*made)
+    return (out, lse) if return_lse else out
+
+
+def cross_attn_bwd(dout, q, k, v, out, lse, kv_len=None, key_mask=None, dq=None, dk=None, dv=None, workspace=None,
+                   stream=None):
+    """(dq, dk, dv) of cross_attn_fwd from the gradient of its output, with its
+    out, lse and mask.  dk and dv are sums over the query heads that share a
+    key head."""
+    _same_kind(dout, q, k, v, out, *(t for t in (dq, dk, dv) if t is not None))
+    code = _dtype_code(q)
+    b, h, hk, Lq, Lk, d = _cross_shapes(q, k, v, kv_len, key_mask)
+    for x, y in ((dout, q), (out, q), (dq, q), (dk, k), (dv, v)):
+        if x is not None and x.shape != y.shape:
+            raise ValueError("dout, out and dq have the shape of q, dk and dv those of k and v")
+    if lse.dtype != torch.float32 or lse.shape != (b, h, Lq) or not lse.is_contiguous() or lse.device != q.device:
+        raise ValueError("lse must be contiguous float32 [b,h,Lq] on the same device")
+    masked = 0 if kv_len is None and key_mask is None else 1
+    on = _LaunchOn(q.device, stream)
+    with on as st:
+        made = []
+        if dq is None:
+            dq = _like(q)
+            made.append(dq)
+        if dk is None:
+            dk = _like(k)
+            made.append(dk)
+        if dv is None:
+            dv = _like(v)
+            made.append(dv)
+        ws = _workspace(_lib_cross_ws(code, b, h, hk, Lq, Lk, d, masked, 1), q.device, workspace)
+        _check(_lib_cross_bwd(_ptr(dout), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(dq), _ptr(dk),
+                              _ptr(dv), code, b, h, hk, Lq, Lk, d, _strides(dout, q, k, v, out, dq, dk, dv),
+                              _ptr(kv_len), _ptr(key_mask), _ptr(ws), ws.numel(), st), "pisa_cross_attn_bwd")
+    on.keep(*made)
+    return dq, dk, dv
 
 
 def launches(entry: str, dtype: torch.dtype = torch.bfloat16) -> int:

@@ -1,0 +1,306 @@
+// Host side of the operators around the self-attention of a transformer
+// block: rotary positions and cross-attention.  Argument checks, workspace
+// carve-up, launch shapes.  Included by pisa_api.cu, whose helpers it uses.
+#pragma once
+
+namespace pisa {
+namespace {
+
+// Strides in force for a [batch, heads, rows, d] tensor: the caller's, dense
+// ones where there are none, and harmless ones for dimensions of size 1.
+HeadView view_of(const pisa_strides* s, int batch, int heads, int rows, int d) {
+  HeadView v{(int64_t)heads * rows * d, (int64_t)rows * d, d};
+  if (s != nullptr) {
+    if (rows > 1) v.r = s->row;
+    if (heads > 1) v.h = s->head;
+    if (batch > 1) v.b = s->batch;
+  }
+  if (rows == 1) v.r = d;
+  if (heads == 1) v.h = d;
+  if (batch == 1) v.b = d;
+  return v;
+}
+
+// Within what 64-bit offsets and tensor maps hold, and no two rows the same.
+bool strides_in_range(const HeadView& v, int d) {
+  constexpr int64_t most = 1LL << 38;
+  return v.b >= d && v.h >= d && v.r >= d && v.b < most && v.h < most && v.r < most;
+}
+
+bool strides_of_16_bytes(const HeadView& v, size_t es) {
+  const int64_t m = (int64_t)(16 / es);
+  return v.b % m == 0 && v.h % m == 0 && v.r % m == 0;
+}
+
+bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// ------------------------------------------------------------------ rotary positions
+
+pisa_status make_rope_plan(int axes, const int* axis_dim, double theta, pisa_rope_layout layout,
+                           pisa_rope_scaling scaling, double factor, int original_len, pisa_rope_plan* plan) {
+  if (plan == nullptr || axis_dim == nullptr || axes < 1 || axes > PISA_ROPE_MAX_AXES) return PISA_ERR_INVALID_ARG;
+  if (layout != PISA_ROPE_INTERLEAVED && layout != PISA_ROPE_HALF) return PISA_ERR_INVALID_ARG;
+  if (scaling < PISA_ROPE_SCALE_NONE || scaling > PISA_ROPE_SCALE_YARN) return PISA_ERR_INVALID_ARG;
+  if (!std::isfinite(theta) || theta <= 0.0) return PISA_ERR_INVALID_ARG;
+  if (scaling != PISA_ROPE_SCALE_NONE && (!std::isfinite(factor) || factor < 1.0)) return PISA_ERR_INVALID_ARG;
+  if (scaling == PISA_ROPE_SCALE_YARN && original_len < 1) return PISA_ERR_INVALID_ARG;
+  pisa_rope_plan p{};
+  p.layout = layout;
+  p.axes = axes;
+  p.magnitude = scaling == PISA_ROPE_SCALE_YARN ? (float)(0.1 * std::log(factor) + 1.0) : 1.0f;
+  for (int a = 0; a < axes; ++a) {
+    const int D = axis_dim[a];
+    if (D < 2 || D % 2 != 0 || D > 2 * PISA_ROPE_MAX_PAIRS - 2 * p.pairs) return PISA_ERR_INVALID_ARG;
+    if (scaling == PISA_ROPE_SCALE_NTK && D == 2) return PISA_ERR_INVALID_ARG;
+    const double base = scaling == PISA_ROPE_SCALE_NTK ? theta * std::pow(factor, D / (D - 2.0)) : theta;
+    for (int i = 0; i < D / 2; ++i) {
+      double f = std::pow(base, -2.0 * i / D);
+      if (scaling == PISA_ROPE_SCALE_LINEAR) f /= factor;
+      if (scaling == PISA_ROPE_SCALE_YARN) {
+        const double turns = original_len * f / 6.283185307179586476925;
+        const double keep = std::fmin(1.0, std::fmax(0.0, (turns - 1.0) / 31.0));
+        f = f * keep + f / factor * (1.0 - keep);
+      }
+      if (!std::isfinite(f)) return PISA_ERR_INVALID_ARG;
+      p.freq[p.pairs] = f;
+      p.axis[p.pairs] = (unsigned char)a;
+      ++p.pairs;
+    }
+  }
+  *plan = p;
+  return PISA_OK;
+}
+
+bool rope_plan_ok(const pisa_rope_plan* p) {
+  if (p == nullptr || (p->layout != PISA_ROPE_INTERLEAVED && p->layout != PISA_ROPE_HALF)) return false;
+  if (p->axes < 1 || p->axes > PISA_ROPE_MAX_AXES || p->pairs < 1 || p->pairs > PISA_ROPE_MAX_PAIRS) return false;
+  if (!std::isfinite(p->magnitude)) return false;
+  for (int i = 0; i < p->pairs; ++i)
+    if (!std::isfinite(p->freq[i]) || p->axis[i] >= p->axes) return false;
+  return true;
+}
+
+template <typename T, bool HALF, int V>
+pisa_status launch_rope(const RopeArgs& a, int batch, cudaStream_t st) {
+  const int tokens = kRopeThreads / (a.d / (HALF ? 2 * V : V));
+  const int gx = (a.L + tokens - 1) / tokens, rows = a.q.heads + a.k.heads;
+  // Head groups: enough blocks for eight per SM (2048 threads), no more, since
+  // each group forms the angles again.
+  const long long want = (8LL * kSMs + (long long)gx * batch - 1) / ((long long)gx * batch);
+  const int gy = (int)(want < 1 ? 1 : want > rows ? rows : want);
+  rope_kernel<T, HALF, V><<<dim3(gx, gy, batch), kRopeThreads, 0, st>>>(a);
+  return last_launch();
+}
+
+// V: 16 bytes where every access is aligned and no unit mixes turned and
+// copied elements, one pair otherwise.
+template <typename T>
+pisa_status run_rope(const RopeArgs& a, bool half, bool wide, int batch, cudaStream_t st) {
+  constexpr int W = 16 / sizeof(T);
+  if (half) return wide ? launch_rope<T, true, W>(a, batch, st) : launch_rope<T, true, 1>(a, batch, st);
+  return wide ? launch_rope<T, false, W>(a, batch, st) : launch_rope<T, false, 2>(a, batch, st);
+}
+
+pisa_status rope_api(const void* q, void* q_out, const void* k, void* k_out, pisa_dtype dtype, int batch, int heads,
+                     int kv_heads, int L, int d, const pisa_strides* strides, const float* positions,
+                     int64_t positions_batch_stride, const pisa_rope_plan* plan, int backward, cudaStream_t st) {
+  if (!valid_dtype(dtype) || !rope_plan_ok(plan)) return PISA_ERR_INVALID_ARG;
+  const int hk = k == nullptr ? 0 : kv_heads;
+  if (batch < 1 || heads < 1 || L < 1 || (k != nullptr && kv_heads < 1)) return PISA_ERR_INVALID_ARG;
+  if ((d != 64 && d != 128) || 2 * plan->pairs > d) return PISA_ERR_UNSUPPORTED;
+  if (batch > 65535 || heads > 65535 || hk > 65535) return PISA_ERR_UNSUPPORTED;
+  const size_t es = dtype == PISA_BF16 ? 2 : 4;
+  if (q == nullptr || q_out == nullptr || (k == nullptr) != (k_out == nullptr)) return PISA_ERR_INVALID_ARG;
+  if (positions == nullptr || !aligned_to(positions, 4)) return PISA_ERR_INVALID_ARG;
+  if (positions_batch_stride < 0 || positions_batch_stride > (1LL << 38)) return PISA_ERR_INVALID_ARG;
+  const void* ptr[4] = {q, q_out, k, k_out};
+  HeadView v[4];
+  bool wide = plan->pairs % (plan->layout == PISA_ROPE_HALF ? 16 / es : 8 / es) == 0;
+  for (int i = 0; i < (k == nullptr ? 2 : 4); ++i) {
+    v[i] = view_of(strides == nullptr ? nullptr : strides + i, batch, i < 2 ? heads : hk, L, d);
+    if (!aligned_to(ptr[i], es) || !strides_in_range(v[i], d)) return PISA_ERR_INVALID_ARG;
+    wide = wide && aligned16(ptr[i]) && strides_of_16_bytes(v[i], es);
+  }
+  RopeArgs a{};
+  a.q = RopeTensor{q, q_out, v[0].b, v[0].h, v[0].r, v[1].b, v[1].h, v[1].r, heads};
+  if (k != nullptr) a.k = RopeTensor{k, k_out, v[2].b, v[2].h, v[2].r, v[3].b, v[3].h, v[3].r, hk};
+  a.pos = positions;
+  a.pos_batch = batch == 1 ? 0 : positions_batch_stride;
+  a.L = L;
+  a.d = d;
+  a.axes = plan->axes;
+  a.pairs = plan->pairs;
+  a.sign = backward ? -1.f : 1.f;
+  a.magnitude = plan->magnitude;
+  for (int i = 0; i < plan->pairs; ++i) {
+    a.freq[i] = plan->freq[i];
+    a.axis[i] = plan->axis[i];
+  }
+  NvtxRange range("pisa.rope");
+  const bool half = plan->layout == PISA_ROPE_HALF;
+  return dtype == PISA_BF16 ? run_rope<__nv_bfloat16>(a, half, wide, batch, st) : run_rope<float>(a, half, wide, batch, st);
+}
+
+// ------------------------------------------------------------------ cross-attention
+
+struct CrossShape {
+  pisa_dtype dtype;
+  int batch, heads, kv_heads, Lq, Lk, d;
+  bool masked;
+  size_t es() const { return dtype == PISA_BF16 ? 2 : 4; }
+};
+
+pisa_status check_cross(const CrossShape& s) {
+  if (!valid_dtype(s.dtype)) return PISA_ERR_INVALID_ARG;
+  if (s.batch < 1 || s.heads < 1 || s.kv_heads < 1 || s.Lq < 1 || s.Lk < 1 || s.heads % s.kv_heads != 0)
+    return PISA_ERR_INVALID_ARG;
+  if (s.d != 64 && s.d != 128) return PISA_ERR_UNSUPPORTED;
+  if ((long long)s.batch * s.heads > 65535) return PISA_ERR_UNSUPPORTED;
+  const long long rows = s.Lq > s.Lk ? s.Lq : s.Lk;
+  if (rows > (1 << 30) || rows * s.d * s.batch * s.heads > (1LL << 40)) return PISA_ERR_UNSUPPORTED;
+  return PISA_OK;
+}
+
+struct CrossFwdPlan {
+  size_t total;
+};
+CrossFwdPlan cross_fwd_plan(const CrossShape&) { return CrossFwdPlan{16}; }
+
+struct CrossBwdPlan {
+  int splits;
+  size_t delta, part, total;
+};
+
+// Query shares per key tile: enough CTAs for two per SM, at least eight query
+// tiles each, and partials of at most 256 MB.
+CrossBwdPlan cross_bwd_plan(const CrossShape& s) {
+  CrossBwdPlan p{};
+  const long long ctas = (long long)s.batch * s.kv_heads * ((s.Lk + 63) / 64);
+  const long long tiles = (long long)(s.heads / s.kv_heads) * ((s.Lq + 31) / 32);
+  const long long one = 2LL * s.batch * s.kv_heads * s.Lk * s.d * sizeof(float);
+  long long n = (2LL * kSMs + ctas - 1) / ctas;
+  if (n > tiles / 8) n = tiles / 8;
+  if (n > (256LL << 20) / one) n = (256LL << 20) / one;
+  p.splits = (int)(n < 1 ? 1 : n);
+  p.delta = align_up((size_t)s.batch * s.heads * s.Lq * sizeof(float));
+  p.part = p.splits > 1 ? align_up((size_t)p.splits * one) : 0;
+  p.total = p.delta + p.part;
+  return p;
+}
+
+// Checks `n` tensors: v[i] gets the strides in force.  shape[i]: 'q' for
+// [batch, heads, Lq, d], 'k' for [batch, kv_heads, Lk, d].
+bool cross_tensors_ok(const CrossShape& s, const void* const* ptr, const char* shape, int n,
+                      const pisa_strides* strides, HeadView* v) {
+  for (int i = 0; i < n; ++i) {
+    if (ptr[i] == nullptr || !aligned16(ptr[i])) return false;
+    v[i] = view_of(strides == nullptr ? nullptr : strides + i, s.batch, shape[i] == 'q' ? s.heads : s.kv_heads,
+                   shape[i] == 'q' ? s.Lq : s.Lk, s.d);
+    if (!strides_in_range(v[i], s.d) || !strides_of_16_bytes(v[i], s.es())) return false;
+  }
+  return true;
+}
+
+CrossArgs cross_args(const CrossShape& s, const int32_t* kv_len, const uint8_t* key_mask) {
+  CrossArgs a{};
+  a.kv_len = kv_len;
+  a.key_mask = key_mask;
+  a.batch = s.batch;
+  a.heads = s.heads;
+  a.kv_heads = s.kv_heads;
+  a.Lq = s.Lq;
+  a.Lk = s.Lk;
+  a.scale = 1.0f / sqrtf((float)s.d);
+  return a;
+}
+
+template <typename T, int D>
+struct CrossFwdOp {
+  static pisa_status run(const CrossArgs& a, const CrossShape& s, cudaStream_t st) {
+    constexpr int BM = 64;
+    const size_t smem = CrossFwdSimt<D, BM>::bytes();
+    if (!set_smem(cross_fwd_simt_kernel<T, D, BM>, smem)) return PISA_ERR_CUDA;
+    cross_fwd_simt_kernel<T, D, BM><<<dim3((s.Lq + BM - 1) / BM, s.batch * s.heads), kCrossThreads, smem, st>>>(a);
+    return last_launch();
+  }
+};
+
+template <typename T, int D>
+struct CrossBwdOp {
+  static pisa_status run(const CrossArgs& a, const CrossShape& s, cudaStream_t st) {
+    const size_t s1 = CrossBwdSimt<D>::dq_bytes(), s2 = CrossBwdSimt<D>::dkv_bytes();
+    if (!set_smem(cross_dq_simt_kernel<T, D>, s1) || !set_smem(cross_dkv_simt_kernel<T, D>, s2)) return PISA_ERR_CUDA;
+    cross_dq_simt_kernel<T, D><<<dim3((s.Lq + 63) / 64, s.batch * s.heads), kCrossThreads, s1, st>>>(a);
+    if (last_launch() != PISA_OK) return PISA_ERR_CUDA;
+    cross_dkv_simt_kernel<T, D>
+        <<<dim3((s.Lk + 63) / 64, s.batch * s.kv_heads, a.splits), kCrossThreads, s2, st>>>(a);
+    if (last_launch() != PISA_OK || a.splits == 1) return last_launch();
+    const long long n = (long long)s.batch * s.kv_heads * s.Lk * D / 4;
+    cross_dkv_sum_kernel<T, D><<<dim3((unsigned)((n + 255) / 256), 2), 256, 0, st>>>(a);
+    return last_launch();
+  }
+};
+
+pisa_status cross_fwd_api(const void* q, const void* k, const void* v, void* out, float* lse, const CrossShape& s,
+                          const pisa_strides* strides, const int32_t* kv_len, const uint8_t* key_mask, void* ws,
+                          size_t ws_bytes, cudaStream_t st) {
+  if (pisa_status e = check_cross(s)) return e;
+  const void* ptr[4] = {q, k, v, out};
+  HeadView w[4];
+  if (!cross_tensors_ok(s, ptr, "qkkq", 4, strides, w)) return PISA_ERR_INVALID_ARG;
+  if (!aligned_to(lse, 4) || !aligned_to(kv_len, 4)) return PISA_ERR_INVALID_ARG;
+  if (ws == nullptr || ws_bytes < cross_fwd_plan(s).total) return PISA_ERR_WORKSPACE;
+  if (!aligned16(ws)) return PISA_ERR_INVALID_ARG;
+  CrossArgs a = cross_args(s, kv_len, key_mask);
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.out = out;
+  a.lse = lse;
+  a.sq = w[0];
+  a.sk = w[1];
+  a.sv = w[2];
+  a.so = w[3];
+  NvtxRange range("pisa.cross_fwd");
+  return dispatch<CrossFwdOp>(s.dtype, s.d, a, s, st);
+}
+
+pisa_status cross_bwd_api(const void* dout, const void* q, const void* k, const void* v, const void* out,
+                          const float* lse, void* dq, void* dk, void* dv, const CrossShape& s,
+                          const pisa_strides* strides, const int32_t* kv_len, const uint8_t* key_mask, void* ws,
+                          size_t ws_bytes, cudaStream_t st) {
+  if (pisa_status e = check_cross(s)) return e;
+  const void* ptr[8] = {dout, q, k, v, out, dq, dk, dv};
+  HeadView w[8];
+  if (!cross_tensors_ok(s, ptr, "qqkkqqkk", 8, strides, w)) return PISA_ERR_INVALID_ARG;
+  if (lse == nullptr || !aligned_to(lse, 4) || !aligned_to(kv_len, 4)) return PISA_ERR_INVALID_ARG;
+  const CrossBwdPlan p = cross_bwd_plan(s);
+  if (ws == nullptr || ws_bytes < p.total) return PISA_ERR_WORKSPACE;
+  if (!aligned16(ws)) return PISA_ERR_INVALID_ARG;
+  CrossArgs a = cross_args(s, kv_len, key_mask);
+  a.g = dout;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.o = out;
+  a.dq = dq;
+  a.dk = dk;
+  a.dv = dv;
+  a.lse = const_cast<float*>(lse);
+  a.sg = w[0];
+  a.sq = w[1];
+  a.sk = w[2];
+  a.sv = w[3];
+  a.so = w[4];
+  a.sdq = w[5];
+  a.sdk = w[6];
+  a.sdv = w[7];
+  a.splits = p.splits;
+  a.delta = reinterpret_cast<float*>(ws);
+  a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + p.delta);
+  NvtxRange range("pisa.cross_bwd");
+  return dispatch<CrossBwdOp>(s.dtype, s.d, a, s, st);
+}
+
+}  // namespace
+}  // namespace pisa

@@ -12,8 +12,10 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include "common.cuh"
+#include "cross_simt.cuh"
 #include "fused_simt.cuh"
 #include "fused_sm100.cuh"
+#include "rope.cuh"
 #include "route_variants.cuh"
 #include "select.cuh"
 #include "select_sm100.cuh"
@@ -728,6 +730,8 @@ pisa_status pick(const TuneKey& key, Tuning* t, int Tuning::*field, const int* c
 }  // namespace
 }  // namespace pisa
 
+#include "block_ops_api.cuh"
+
 using namespace pisa;
 
 extern "C" {
@@ -1068,6 +1072,46 @@ pisa_status pisa_tuning_load(const char* path) {
   std::lock_guard<std::mutex> lock(g_tune_mutex);
   for (const auto& kv : got) g_tune[kv.first] = kv.second;
   return PISA_OK;
+}
+
+pisa_status pisa_rope_make_plan(int axes, const int* axis_dim, double theta, pisa_rope_layout layout,
+                                pisa_rope_scaling scaling, double factor, int original_len,
+                                pisa_rope_plan* plan) {
+  return make_rope_plan(axes, axis_dim, theta, layout, scaling, factor, original_len, plan);
+}
+
+pisa_status pisa_rope(const void* q, void* q_out, const void* k, void* k_out, pisa_dtype dtype, int batch,
+                      int heads, int kv_heads, int L, int d, const pisa_strides* strides,
+                      const float* positions, int64_t positions_batch_stride, const pisa_rope_plan* plan,
+                      int backward, void* stream) {
+  return rope_api(q, q_out, k, k_out, dtype, batch, heads, kv_heads, L, d, strides, positions,
+                  positions_batch_stride, plan, backward, (cudaStream_t)stream);
+}
+
+size_t pisa_cross_workspace_size(pisa_dtype dtype, int batch, int heads, int kv_heads, int Lq, int Lk, int d,
+                                 int masked, int backward) {
+  const CrossShape s{dtype, batch, heads, kv_heads, Lq, Lk, d, masked != 0};
+  if (check_cross(s) != PISA_OK) return 0;
+  return backward ? cross_bwd_plan(s).total : cross_fwd_plan(s).total;
+}
+
+pisa_status pisa_cross_attn_fwd(const void* q, const void* k, const void* v, void* out, float* lse,
+                                pisa_dtype dtype, int batch, int heads, int kv_heads, int Lq, int Lk, int d,
+                                const pisa_strides* strides, const int32_t* kv_len, const uint8_t* key_mask,
+                                void* workspace, size_t workspace_bytes, void* stream) {
+  const CrossShape s{dtype, batch, heads, kv_heads, Lq, Lk, d, kv_len != nullptr || key_mask != nullptr};
+  return cross_fwd_api(q, k, v, out, lse, s, strides, kv_len, key_mask, workspace, workspace_bytes,
+                       (cudaStream_t)stream);
+}
+
+pisa_status pisa_cross_attn_bwd(const void* dout, const void* q, const void* k, const void* v, const void* out,
+                                const float* lse, void* dq, void* dk, void* dv, pisa_dtype dtype, int batch,
+                                int heads, int kv_heads, int Lq, int Lk, int d, const pisa_strides* strides,
+                                const int32_t* kv_len, const uint8_t* key_mask, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+  const CrossShape s{dtype, batch, heads, kv_heads, Lq, Lk, d, kv_len != nullptr || key_mask != nullptr};
+  return cross_bwd_api(dout, q, k, v, out, lse, dq, dk, dv, s, strides, kv_len, key_mask, workspace,
+                       workspace_bytes, (cudaStream_t)stream);
 }
 
 pisa_status pisa_set_wait_limit(uint64_t limit_ns, void* stream) {

@@ -1,0 +1,154 @@
+"""Refusals and host arithmetic of the rotary positions and the
+cross-attention (no GPU: every check comes before the first CUDA call)."""
+
+import ctypes
+import math
+
+import pytest
+import torch
+
+from block_ops_ref import rope_freqs
+
+FAKE = ctypes.c_void_p(0x10000)  # never dereferenced: validation fails first
+MISALIGNED = ctypes.c_void_p(0x10008)
+ODD = ctypes.c_void_p(0x10001)
+
+
+@pytest.mark.parametrize("dims", [(128,), (16, 56, 56), (44, 42, 42), (4,)])
+@pytest.mark.parametrize("scaling,factor,original", [("none", 1, 0), ("linear", 2.5, 0), ("ntk", 4, 0),
+                                                     ("yarn", 8, 4096), ("yarn", 1, 1)])
+def test_plan_frequencies(lib, dims, scaling, factor, original):
+    plan = lib._rope_plan(dims, 10000.0, "half", scaling, float(factor), original)
+    f, axis, m = rope_freqs(dims, 10000.0, scaling, float(factor), original)
+    assert plan.pairs == len(f) and plan.axes == len(dims) and list(plan.axis)[:len(f)] == axis
+    for x, y in zip(plan.freq, f):
+        assert abs(x - y) <= 1e-14 * y
+    assert abs(plan.magnitude - m) <= 2.0 ** -23 * m
+
+
+def test_scaling_ends(lib):
+    """NTK: the fastest pair keeps its speed, the slowest is slowed by the
+    factor.  By parts: the fastest pairs keep theirs, the slowest are divided."""
+    plain = lib._rope_plan((128,), 10000.0, "half", "none", 1.0, 0)
+    ntk = lib._rope_plan((128,), 10000.0, "half", "ntk", 4.0, 0)
+    yarn = lib._rope_plan((128,), 10000.0, "half", "yarn", 4.0, 4096)
+    assert ntk.freq[0] == yarn.freq[0] == plain.freq[0] == 1.0
+    assert math.isclose(ntk.freq[63], plain.freq[63] / 4, rel_tol=1e-12)
+    assert math.isclose(yarn.freq[63], plain.freq[63] / 4, rel_tol=1e-12)
+
+
+@pytest.mark.parametrize("args", [
+    ((), 1e4, "half", "none", 1.0, 0), ((3,), 1e4, "half", "none", 1.0, 0), ((0,), 1e4, "half", "none", 1.0, 0),
+    ((2, 2, 2, 2), 1e4, "half", "none", 1.0, 0), ((128, 2), 1e4, "half", "none", 1.0, 0),
+    ((64,), 0.0, "half", "none", 1.0, 0), ((64,), float("nan"), "half", "none", 1.0, 0),
+    ((64,), 1e4, "half", "linear", 0.5, 0), ((64,), 1e4, "half", "ntk", float("inf"), 0),
+    ((2,), 1e4, "half", "ntk", 2.0, 0), ((64,), 1e4, "half", "yarn", 2.0, 0)])
+def test_plans_refused(lib, args):
+    with pytest.raises(lib.PisaError) as e:
+        lib._rope_plan(*args)
+    assert e.value.code == lib.PISA_ERR_INVALID_ARG
+
+
+def test_unknown_names(lib):
+    with pytest.raises(ValueError):
+        lib._rope_plan((64,), 1e4, "spiral", "none", 1.0, 0)
+    with pytest.raises(ValueError):
+        lib._rope_plan((64,), 1e4, "half", "more", 1.0, 0)
+
+
+def test_rope_refuses(lib):
+    raw = lib.raw_lib()
+    plan = lib._rope_plan((64,), 1e4, "half", "none", 1.0, 0)
+    S = lib._Strides
+    dense = (4 * 100 * 64, 100 * 64, 64)
+
+    def call(q=FAKE, qo=FAKE, k=FAKE, ko=FAKE, dtype=0, b=2, h=4, hk=4, L=100, d=64, st=None, pos=FAKE, pb=0, p=plan):
+        return raw.pisa_rope(q, qo, k, ko, dtype, b, h, hk, L, d, st, pos, pb,
+                             None if p is None else ctypes.byref(p), 0, None)
+
+    bad = lib.PISA_ERR_INVALID_ARG
+    for kw in (dict(q=None), dict(qo=None), dict(k=None), dict(ko=None), dict(pos=None), dict(p=None), dict(q=ODD),
+               dict(ko=ODD), dict(pos=ctypes.c_void_p(0x10002)), dict(dtype=2), dict(b=0), dict(h=0), dict(hk=0),
+               dict(L=0), dict(pb=-1)):
+        assert call(**kw) == bad, kw
+    assert call(d=96) == lib.PISA_ERR_UNSUPPORTED
+    assert call(d=64, p=lib._rope_plan((66,), 1e4, "half", "none", 1.0, 0)) == lib.PISA_ERR_UNSUPPORTED
+    assert call(b=70000) == lib.PISA_ERR_UNSUPPORTED
+    for strides in ((0, 6400, 64), (25600, 0, 64), (25600, 6400, 63), (-25600, 6400, 64), (1 << 40, 6400, 64)):
+        assert call(st=(S * 4)(strides, dense, dense, dense)) == bad, strides
+        assert call(st=(S * 4)(dense, dense, dense, strides)) == bad, strides
+    for field, value in (("pairs", 0), ("pairs", 65), ("axes", 0), ("axes", 4), ("layout", 2),
+                         ("magnitude", float("nan"))):
+        other = type(plan).from_buffer_copy(plan)
+        setattr(other, field, value)
+        assert call(p=other) == bad, field
+    other = type(plan).from_buffer_copy(plan)
+    other.axis[31] = 1
+    assert call(p=other) == bad
+    other.axis[31] = 0
+    other.freq[0] = float("inf")
+    assert call(p=other) == bad
+
+
+def test_cross_workspace_sizes(lib):
+    f = lib.cross_workspace_size
+    for dtype in (torch.bfloat16, torch.float32):
+        for masked in (False, True):
+            assert f(dtype, 1, 40, 40, 75600, 512, 128, masked) >= 16
+            assert f(dtype, 1, 40, 40, 75600, 512, 128, masked, backward=True) >= 40 * 75600 * 4
+    assert f(torch.float16, 1, 4, 4, 100, 100, 64) == 0
+    assert f(torch.float32, 1, 4, 3, 100, 100, 64) == 0
+    assert f(torch.float32, 1, 4, 4, 100, 100, 96) == 0
+    assert f(torch.float32, 1, 4, 4, 0, 100, 64) == 0
+    assert f(torch.float32, 1, 4, 4, 100, 0, 64) == 0
+    assert f(torch.float32, 300, 300, 4, 100, 100, 64) == 0
+
+
+def _cross_calls(lib):
+    raw = lib.raw_lib()
+
+    def fwd(q=FAKE, k=FAKE, v=FAKE, out=FAKE, lse=FAKE, dtype=0, b=2, h=4, hk=2, Lq=100, Lk=50, d=64, st=None,
+            kv_len=None, mask=None, ws=FAKE, n=1 << 40):
+        return raw.pisa_cross_attn_fwd(q, k, v, out, lse, dtype, b, h, hk, Lq, Lk, d, st, kv_len, mask, ws,
+                                       ctypes.c_size_t(n), None)
+
+    def bwd(q=FAKE, k=FAKE, v=FAKE, out=FAKE, lse=FAKE, dtype=0, b=2, h=4, hk=2, Lq=100, Lk=50, d=64, st=None,
+            kv_len=None, mask=None, ws=FAKE, n=1 << 40, dout=FAKE, dq=FAKE, dk=FAKE, dv=FAKE):
+        return raw.pisa_cross_attn_bwd(dout, q, k, v, out, lse, dq, dk, dv, dtype, b, h, hk, Lq, Lk, d, st, kv_len,
+                                       mask, ws, ctypes.c_size_t(n), None)
+
+    return fwd, bwd
+
+
+def test_cross_refuses(lib):
+    fwd, bwd = _cross_calls(lib)
+    bad, S = lib.PISA_ERR_INVALID_ARG, lib._Strides
+    for call in (fwd, bwd):
+        for kw in (dict(q=None), dict(k=None), dict(v=None), dict(out=None), dict(q=MISALIGNED), dict(v=MISALIGNED),
+                   dict(out=MISALIGNED), dict(lse=ODD), dict(kv_len=ODD), dict(dtype=5), dict(b=0), dict(h=0),
+                   dict(hk=0), dict(hk=3), dict(hk=8), dict(Lq=0), dict(Lk=0), dict(ws=MISALIGNED)):
+            assert call(**kw) == bad, (call, kw)
+        assert call(d=80) == lib.PISA_ERR_UNSUPPORTED
+        assert call(b=300, h=300, hk=300) == lib.PISA_ERR_UNSUPPORTED
+        assert call(Lq=(1 << 30) + 1) == lib.PISA_ERR_UNSUPPORTED
+        assert call(ws=None) == lib.PISA_ERR_WORKSPACE
+        assert call(n=8) == lib.PISA_ERR_WORKSPACE
+        rows, keys = (25600, 6400, 64), (6400, 3200, 64)
+        order = [rows, keys, keys, rows] if call is fwd else [rows, rows, keys, keys, rows, rows, keys, keys]
+        for i in range(len(order)):
+            for wrong in ((0, 6400, 64), (25600, 0, 64), (25600, 6400, 0), (25600, 6400, 68), (25601, 6400, 64),
+                          (25600, 6400, 60), (25600, -6400, 64), (1 << 39, 6400, 64)):
+                st = list(order)
+                st[i] = wrong
+                assert call(st=(S * len(st))(*st)) == bad, (call, i, wrong)
+    for kw in (dict(dout=None), dict(dq=None), dict(dk=MISALIGNED), dict(dv=None), dict(lse=None)):
+        assert bwd(**kw) == bad, kw
+
+
+def test_binding_refuses_tensors(lib):
+    """Shapes, types and devices are checked before any launch."""
+    t = torch.zeros(1, 2, 8, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        lib.cross_attn_fwd(t, t, t)  # host tensors
+    with pytest.raises(ValueError):
+        lib.rope(t, t, torch.zeros(8, 1), (64,))

@@ -1,0 +1,154 @@
+"""Rotary positions on the GPU against their 64-bit form."""
+
+import pytest
+import torch
+
+from block_ops_ref import assert_within, rope_ref
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    torch.cuda.init()
+
+
+def _grid(*sizes):
+    axes = torch.meshgrid(*(torch.arange(n, device="cuda", dtype=torch.float32) for n in sizes), indexing="ij")
+    return torch.stack([a.flatten() for a in axes], 1).contiguous()
+
+
+def _x(seed, *shape, dtype=torch.bfloat16):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randn(*shape, device="cuda", generator=g).to(dtype)
+
+
+CASES = [
+    # axis_dims, d, layout, scaling, factor, original
+    ((16, 56, 56), 128, "interleaved", "none", 1.0, 0),
+    ((44, 42, 42), 128, "interleaved", "linear", 2.0, 0),
+    ((44, 42, 42), 128, "half", "ntk", 4.0, 0),
+    ((64,), 64, "half", "yarn", 4.0, 512),
+    ((64,), 128, "half", "none", 1.0, 0),       # half of the head
+    ((32,), 128, "interleaved", "yarn", 8.0, 1024),
+    ((2,), 64, "interleaved", "none", 1.0, 0),  # one pair
+    ((6, 4), 64, "half", "linear", 1.5, 0),     # five pairs: no 16-byte units
+    ((10, 8), 128, "interleaved", "ntk", 2.0, 0),
+    ((4, 4, 6), 64, "half", "ntk", 3.0, 0),
+]
+
+
+@pytest.mark.parametrize("backward", [False, True])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("case", CASES, ids=lambda c: f"{c[0]}-{c[1]}-{c[2]}-{c[3]}".replace(" ", ""))
+def test_against_64_bits(lib, case, dtype, backward):
+    dims, d, layout, scaling, factor, original = case
+    kw = dict(theta=10000.0, layout=layout, scaling=scaling, factor=factor, original_len=original)
+    L = 3 * 5 * 7
+    pos = _grid(*{1: (L,), 2: (7, 15), 3: (3, 5, 7)}[len(dims)]) + 11
+    q, k = _x(1, 2, 6, L, d, dtype=dtype), _x(2, 2, 3, L, d, dtype=dtype)
+    f = lib.rope_bwd if backward else lib.rope
+    got = f(q, k, pos, dims, **kw)
+    for x, y, name in zip((q, k), got, "qk"):
+        assert y.is_contiguous() and y.dtype == dtype
+        assert_within(y, rope_ref(x, pos, dims, backward=backward, **kw), name)
+
+
+@pytest.mark.parametrize("L", [1, 2, 31, 33, 1000])
+@pytest.mark.parametrize("h,hk", [(1, 1), (5, 1), (40, 8)])
+def test_lengths_and_heads(lib, L, h, hk):
+    pos = _grid(L)
+    q, k = _x(3, 1, h, L, 128), _x(4, 1, hk, L, 128)
+    for x, y in zip((q, k), lib.rope(q, k, pos, (128,))):
+        assert_within(y, rope_ref(x, pos, (128,)), f"L={L}")
+
+
+def test_far_and_fractional_positions(lib):
+    """Angles of millions of turns, negative and fractional positions."""
+    pos = torch.tensor([[0.0], [-3.5], [1e6 + 0.5], [16777215.0], [-16777216.0], [2.0 ** 30]], device="cuda")
+    q = _x(5, 1, 2, 6, 128, dtype=torch.float32)
+    (y, none) = lib.rope(q, None, pos, (128,))
+    assert none is None
+    assert_within(y, rope_ref(q, pos, (128,)), "far")
+
+
+def test_positions_of_each_batch_entry(lib):
+    pos = torch.stack([_grid(50), _grid(50) * 3 + 7])
+    q, k = _x(6, 2, 3, 50, 64), _x(7, 2, 3, 50, 64)
+    for x, y in zip((q, k), lib.rope(q, k, pos, (64,), layout="half")):
+        assert_within(y, rope_ref(x, pos, (64,), layout="half"), "batch positions")
+
+
+@pytest.mark.parametrize("layout", ["interleaved", "half"])
+def test_strides_in_place_and_rows_around(lib, layout):
+    """Reads a slice of a fused projection, writes into a slice of another
+    buffer (what lies around it stays), and in place."""
+    b, L, h, d = 2, 77, 4, 64
+    qkv = _x(8, b, L, 3, h, d)
+    q, k = (qkv[:, :, i].permute(0, 2, 1, 3) for i in (0, 1))
+    pos = _grid(7, 11)
+    buf = torch.full((b, L + 5, 2, h, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    qo, ko = (buf[:, 2:L + 2, i].permute(0, 2, 1, 3) for i in (0, 1))
+    lib.rope(q, k, pos, (32, 32), layout=layout, q_out=qo, k_out=ko)
+    refs = [rope_ref(x, pos, (32, 32), layout=layout) for x in (q, k)]
+    for y, ref in zip((qo, ko), refs):
+        assert_within(y, ref, "strided")
+    assert (buf[:, :2] == 7).all() and (buf[:, L + 2:] == 7).all()
+    v = qkv[:, :, 2].clone()
+    lib.rope(q, k, pos, (32, 32), layout=layout, q_out=q, k_out=k)
+    for y, ref in zip((q, k), refs):
+        assert_within(y, ref, "in place")
+    assert torch.equal(qkv[:, :, 2], v)
+
+
+@pytest.mark.parametrize("layout", ["interleaved", "half"])
+def test_unaligned_views(lib, layout):
+    """Rows that start off a 16-byte boundary take the narrow accesses."""
+    wide = _x(9, 1, 3, 40, 67)
+    q = wide[..., 3:]
+    pos = _grid(40)
+    y, _ = lib.rope(q, None, pos, (64,), layout=layout)
+    assert_within(y, rope_ref(q, pos, (64,), layout=layout), "unaligned")
+
+
+def test_round_trip_and_gradient_by_differences(lib):
+    """The backward map undoes the forward one (an orthogonal map, m = 1), and
+    is its gradient: <rope(x + h e), g> - <rope(x - h e), g> = 2h <e, rope_bwd(g)>."""
+    pos = _grid(8, 9)
+    kw = dict(axis_dims=(24, 40), layout="half")
+    x, g, e = (_x(s, 1, 2, 72, 64, dtype=torch.float32) for s in (10, 11, 12))
+    y, _ = lib.rope(x, None, pos, **kw)
+    back, _ = lib.rope_bwd(y, None, pos, **kw)
+    # two maps of at most 2^-21 (|u| + |w|) <= 2^-20 max|x| error each
+    assert (back - x).abs().max() <= 2.0 ** -18 * x.abs().max()
+    kw.update(scaling="yarn", factor=4.0, original_len=16)
+    h = 0.5
+    up, _ = lib.rope(x + h * e, None, pos, **kw)
+    down, _ = lib.rope(x - h * e, None, pos, **kw)
+    gx, _ = lib.rope_bwd(g, None, pos, **kw)
+    lhs = ((up.double() - down.double()) * g.double()).sum() / (2 * h)
+    rhs = (gx.double() * e.double()).sum()
+    # the map is linear, so only rounding is left: 9216 terms, each within
+    # 2^-19 of products of entries below 6
+    assert abs(lhs - rhs) <= 2.0 ** -19 * 72 * 64 * 2 * 36
+
+
+def test_side_stream_and_graph(lib):
+    pos = _grid(100)
+    q, k = _x(13, 1, 4, 100, 128), _x(14, 1, 4, 100, 128)
+    want = lib.rope(q, k, pos, (128,))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = lib.rope(q, k, pos, (128,), stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert all(torch.equal(x, y) for x, y in zip(want, got))
+    qo, ko = torch.empty_like(q), torch.empty_like(k)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        lib.rope(q, k, pos, (128,), q_out=qo, k_out=ko)
+    new = _x(15, 1, 4, 100, 128)
+    q.copy_(new)
+    graph.replay()
+    assert torch.equal(qo, lib.rope(new, None, pos, (128,))[0]) and torch.equal(ko, want[1])

@@ -161,10 +161,49 @@ pisa_status check_cross(const CrossShape& s) {
   return PISA_OK;
 }
 
-struct CrossFwdPlan {
-  size_t total;
+// Allowed keys packed for the tensor cores (bf16 with a mask).
+struct CrossPackPlan {
+  int padded;
+  size_t tile, count, place, total;  // bytes: one of keys / values, counts, places
 };
-CrossFwdPlan cross_fwd_plan(const CrossShape&) { return CrossFwdPlan{16}; }
+CrossPackPlan cross_pack_plan(const CrossShape& s, bool backward) {
+  CrossPackPlan p{};
+  if (!s.masked || s.dtype != PISA_BF16) return p;
+  p.padded = (s.Lk + 127) / 128 * 128;
+  p.tile = align_up((size_t)s.batch * s.kv_heads * p.padded * s.d * 2);
+  p.count = align_up((size_t)s.batch * sizeof(int32_t));
+  p.place = backward ? align_up((size_t)s.batch * s.Lk * sizeof(int32_t)) : 0;
+  p.total = 2 * p.tile + p.count + p.place;
+  return p;
+}
+
+struct CrossFwdPlan {
+  CrossPackPlan pack;
+  int pairs, splits;
+  size_t part, part_lse, total;
+};
+
+// Tensor-core forward: shares of the keys where the pairs of query tiles leave
+// at least half of the SMs without work (each share re-reads its query tiles
+// and its output goes through memory in 32 bits, which a few rows can afford).
+CrossFwdPlan cross_fwd_plan(const CrossShape& s) {
+  CrossFwdPlan p{};
+  p.splits = 1;
+  if (s.dtype == PISA_BF16) {
+    p.pack = cross_pack_plan(s, false);
+    p.pairs = ((s.Lq + 127) / 128 + 1) / 2;
+    const long long items = (long long)s.batch * s.heads * p.pairs, tiles = (s.Lk + 127) / 128;
+    if (2 * items <= kSMs && tiles > 1) p.splits = (int)(kSMs / items < tiles ? kSMs / items : tiles);
+    if (p.splits > 1) {
+      const size_t rows = (size_t)p.splits * s.batch * s.heads * s.Lq;
+      p.part = align_up(rows * s.d * sizeof(float));
+      p.part_lse = align_up(rows * sizeof(float));
+    }
+  }
+  p.total = p.pack.total + p.part + p.part_lse;
+  if (p.total < 16) p.total = 16;
+  return p;
+}
 
 struct CrossBwdPlan {
   int splits;
@@ -214,14 +253,94 @@ CrossArgs cross_args(const CrossShape& s, const int32_t* kv_len, const uint8_t* 
   return a;
 }
 
+// Packs the allowed keys (bf16): fills the maps, the count and, for the
+// backward pass, the places; without a mask the maps are those of k and v.
+template <int D>
+pisa_status run_cross_pack(const CrossArgs& a, const CrossShape& s, const CrossPackPlan& p, char* ws, CUtensorMap* mK,
+                           CUtensorMap* mV, const int32_t** count, const int32_t** place, cudaStream_t st) {
+  *count = *place = nullptr;
+  if (!s.masked)
+    return make_map_view(mK, a.k, D, s.Lk, s.kv_heads, s.batch, a.sk) &&
+                   make_map_view(mV, a.v, D, s.Lk, s.kv_heads, s.batch, a.sv)
+               ? PISA_OK
+               : PISA_ERR_CUDA;
+  CrossPackArgs c{};
+  c.k = a.k;
+  c.v = a.v;
+  c.sk = a.sk;
+  c.sv = a.sv;
+  c.kv_len = a.kv_len;
+  c.key_mask = a.key_mask;
+  c.pk = reinterpret_cast<__nv_bfloat16*>(ws);
+  c.pv = reinterpret_cast<__nv_bfloat16*>(ws + p.tile);
+  c.count = reinterpret_cast<int32_t*>(ws + 2 * p.tile);
+  c.place = p.place ? reinterpret_cast<int32_t*>(ws + 2 * p.tile + p.count) : nullptr;
+  c.kv_heads = s.kv_heads;
+  c.Lk = s.Lk;
+  c.padded = p.padded;
+  const uint64_t slices = (uint64_t)s.batch * s.kv_heads;
+  const HeadView dense{(int64_t)slices * p.padded * D, (int64_t)p.padded * D, D};
+  if (!make_map_view(mK, c.pk, D, p.padded, slices, 1, dense) || !make_map_view(mV, c.pv, D, p.padded, slices, 1, dense))
+    return PISA_ERR_CUDA;
+  cross_pack_kernel<D><<<dim3(p.padded / kPackRows, (unsigned)slices), kPackThreads, 0, st>>>(c);
+  *count = c.count;
+  *place = c.place;
+  return last_launch();
+}
+
+bool sm_count(int* sms) {
+  int dev = 0;
+  return cudaGetDevice(&dev) == cudaSuccess &&
+         cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess;
+}
+
+template <int D>
+pisa_status run_cross_fwd_sm100(const CrossArgs& a, const CrossShape& s, char* ws, cudaStream_t st) {
+  const CrossFwdPlan p = cross_fwd_plan(s);
+  CUtensorMap mQ, mK, mV;
+  const int32_t *count, *place;
+  if (pisa_status e = run_cross_pack<D>(a, s, p.pack, ws, &mK, &mV, &count, &place, st)) return e;
+  if (!make_map_view(&mQ, a.q, D, s.Lq, s.heads, s.batch, a.sq)) return PISA_ERR_CUDA;
+  CrossFwdArgs f{};
+  f.out = static_cast<__nv_bfloat16*>(a.out);
+  f.so = a.so;
+  f.lse = a.lse;
+  f.count = count;
+  f.part = reinterpret_cast<float*>(ws + p.pack.total);
+  f.part_lse = reinterpret_cast<float*>(ws + p.pack.total + p.part);
+  f.heads = s.heads;
+  f.kv_heads = s.kv_heads;
+  f.Lq = s.Lq;
+  f.Lk = s.Lk;
+  f.BH = s.batch * s.heads;
+  f.pairs = p.pairs;
+  f.splits = p.splits;
+  f.n_items = f.BH * p.pairs * p.splits;
+  f.scale_log2 = kLog2e * a.scale;
+  int sms = 0;
+  if (!sm_count(&sms)) return PISA_ERR_CUDA;
+  const size_t smem = CrossFwdLayout<D>::bytes();
+  if (!set_smem(cross_fwd_sm100_kernel<D>, smem)) return PISA_ERR_CUDA;
+  cross_fwd_sm100_kernel<D><<<f.n_items < sms ? f.n_items : sms, kCrossFwdThreads, smem, st>>>(mQ, mK, mV, f);
+  if (last_launch() != PISA_OK || p.splits == 1) return last_launch();
+  constexpr int rows = 256 / (D / 4);
+  const long long n = ((long long)f.BH * s.Lq + rows - 1) / rows;
+  cross_join_kernel<D><<<(unsigned)n, 256, 0, st>>>(f);
+  return last_launch();
+}
+
 template <typename T, int D>
 struct CrossFwdOp {
-  static pisa_status run(const CrossArgs& a, const CrossShape& s, cudaStream_t st) {
-    constexpr int BM = 64;
-    const size_t smem = CrossFwdSimt<D, BM>::bytes();
-    if (!set_smem(cross_fwd_simt_kernel<T, D, BM>, smem)) return PISA_ERR_CUDA;
-    cross_fwd_simt_kernel<T, D, BM><<<dim3((s.Lq + BM - 1) / BM, s.batch * s.heads), kCrossThreads, smem, st>>>(a);
-    return last_launch();
+  static pisa_status run(const CrossArgs& a, const CrossShape& s, char* ws, cudaStream_t st) {
+    if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+      return run_cross_fwd_sm100<D>(a, s, ws, st);
+    } else {
+      constexpr int BM = 64;
+      const size_t smem = CrossFwdSimt<D, BM>::bytes();
+      if (!set_smem(cross_fwd_simt_kernel<T, D, BM>, smem)) return PISA_ERR_CUDA;
+      cross_fwd_simt_kernel<T, D, BM><<<dim3((s.Lq + BM - 1) / BM, s.batch * s.heads), kCrossThreads, smem, st>>>(a);
+      return last_launch();
+    }
   }
 };
 
@@ -262,7 +381,7 @@ pisa_status cross_fwd_api(const void* q, const void* k, const void* v, void* out
   a.sv = w[2];
   a.so = w[3];
   NvtxRange range("pisa.cross_fwd");
-  return dispatch<CrossFwdOp>(s.dtype, s.d, a, s, st);
+  return dispatch<CrossFwdOp>(s.dtype, s.d, a, s, static_cast<char*>(ws), st);
 }
 
 pisa_status cross_bwd_api(const void* dout, const void* q, const void* k, const void* v, const void* out,

@@ -1,0 +1,529 @@
+// Cross-attention to an encoder's states on the 5th-generation tensor cores
+// (bf16 inputs).  The formulas are those at the head of cross_simt.cuh.
+#pragma once
+
+#include "cross_simt.cuh"
+#include "fused_sm100.cuh"
+#include "sm100.cuh"
+
+namespace pisa {
+
+// ------------------------------------------------------------------ allowed keys, packed
+//
+// With key lengths or a mask, the allowed keys and values are copied once,
+// in order and without gaps, to [batch * kv_heads][padded][D], followed by zero
+// rows to the end of the last 128-row tile.  The attention then knows only a
+// count per batch entry: masked tiles cost nothing, and nothing that stands
+// behind the mask reaches a tensor core, where 0 x NaN would.  Keys are few
+// next to queries, so the copy is small (512 keys of 40 heads: 21 MB, next to
+// 1.5 GB of queries and outputs for 75600 tokens).
+//
+// Grid: (blocks of 64 packed rows, batch * kv_heads).  Each block counts the
+// whole mask row of its batch entry (one byte a key) to find its own keys, so
+// no second launch has to wait for a prefix sum.
+constexpr int kPackRows = 64, kPackThreads = 256;
+
+struct CrossPackArgs {
+  const void *k, *v;
+  HeadView sk, sv;
+  const int32_t* kv_len;
+  const uint8_t* key_mask;
+  __nv_bfloat16 *pk, *pv;
+  int32_t* count;  // [batch]: allowed keys
+  int32_t* place;  // [batch][Lk]: packed row of each key, -1 where not allowed; null when not needed
+  int kv_heads, Lk, padded;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kPackThreads) cross_pack_kernel(const CrossPackArgs a) {
+  __shared__ int warp_sum[kPackThreads / 32];
+  __shared__ int src[kPackRows];
+  const int b = blockIdx.y / a.kv_heads, hk = blockIdx.y % a.kv_heads;
+  const int first = blockIdx.x * kPackRows, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int len = a.kv_len == nullptr ? a.Lk : max(0, min(a.Lk, a.kv_len[b]));
+  const uint8_t* mask = a.key_mask == nullptr ? nullptr : a.key_mask + (int64_t)b * a.Lk;
+  const bool report = blockIdx.x == 0 && hk == 0;
+  int total = len;
+  if (mask == nullptr) {
+    if (threadIdx.x < kPackRows) src[threadIdx.x] = first + threadIdx.x < len ? first + (int)threadIdx.x : -1;
+    if (report && a.place != nullptr)
+      for (int j = threadIdx.x; j < a.Lk; j += kPackThreads) a.place[(int64_t)b * a.Lk + j] = j < len ? j : -1;
+  } else {
+    if (threadIdx.x < kPackRows) src[threadIdx.x] = -1;
+    total = 0;
+    for (int j0 = 0; j0 < a.Lk; j0 += kPackThreads) {
+      const int j = j0 + threadIdx.x;
+      const bool on = j < len && mask[j] != 0;
+      const unsigned ballot = __ballot_sync(0xffffffffu, on);
+      __syncthreads();
+      if (lane == 0) warp_sum[warp] = __popc(ballot);
+      __syncthreads();
+      int before = total;
+      for (int w = 0; w < kPackThreads / 32; ++w) {
+        if (w < warp) before += warp_sum[w];
+        total += warp_sum[w];
+      }
+      const int at = before + __popc(ballot & ((1u << lane) - 1u));
+      if (on && at >= first && at < first + kPackRows) src[at - first] = j;
+      if (report && a.place != nullptr && j < a.Lk) a.place[(int64_t)b * a.Lk + j] = on ? at : -1;
+    }
+  }
+  if (report && threadIdx.x == 0) a.count[b] = total;
+  __syncthreads();
+  const int end = min(kPackRows, (total + 127) / 128 * 128 - first);
+  const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(a.k) + b * a.sk.b + hk * a.sk.h;
+  const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.v) + b * a.sv.b + hk * a.sv.h;
+  const int64_t out = ((int64_t)blockIdx.y * a.padded + first) * D;
+  for (int e = threadIdx.x; e < end * (D / 8); e += kPackThreads) {
+    const int r = e / (D / 8), c = e % (D / 8) * 8;
+    uint4 x = make_uint4(0, 0, 0, 0), y = x;
+    if (src[r] >= 0) {
+      x = *reinterpret_cast<const uint4*>(k + src[r] * a.sk.r + c);
+      y = *reinterpret_cast<const uint4*>(v + src[r] * a.sv.r + c);
+    }
+    *reinterpret_cast<uint4*>(a.pk + out + r * D + c) = x;
+    *reinterpret_cast<uint4*>(a.pv + out + r * D + c) = y;
+  }
+}
+
+// ------------------------------------------------------------------ forward
+//
+// Persistent CTAs, one per SM, walk items: a pair of consecutive 128-row query
+// tiles (A, B) of one head, and, where there are fewer pairs than SMs, one of
+// `splits` shares of that head's key tiles.  Warp roles as in the fused
+// self-attention kernel: warps 0-3 softmax of tile A, 4-7 of tile B (a thread
+// per query row = TMEM lane), warp 8 TMA producer, warp 9 MMA issuer, 10-11
+// idle.  S = Q K^T, then P (bf16, over S in TMEM) and O += P V; both tiles use
+// each key and value tile, loaded once into a ring of four 128-row slots.
+//
+// Text has few keys (4 tiles of 128 for 512), so an item is short and what
+// counts is that items follow each other without a gap: the issuer runs one
+// item's last P V and the next item's first Q K^T back to back, the Q tiles
+// rotate through three buffers (A of the next item is loaded while both tiles
+// of this one are in use; B's takes the buffer that A's last S has left), and
+// a tile's epilogue overlaps the other tile's MMAs.
+//
+// TMEM columns: [0,128) S_A, [128,256) S_B, [256,256+D) O_A, [256+D,256+2D) O_B.
+struct CrossFwdArgs {
+  __nv_bfloat16* out;
+  HeadView so;
+  float* lse;            // [batch * heads][Lq] or null
+  const int32_t* count;  // allowed keys per batch entry, or null: Lk
+  float* part;           // splits > 1: [splits][batch * heads][Lq][D] outputs of each share
+  float* part_lse;       // splits > 1: [splits][batch * heads][Lq], binary logarithms
+  int heads, kv_heads, Lq, Lk, BH, pairs, splits, n_items;
+  float scale_log2;
+};
+
+constexpr int kCrossStages = 4, kCrossQBufs = 3, kCrossFwdThreads = 384;
+
+template <int D>
+struct CrossFwdLayout {
+  static constexpr uint32_t kTile = 128u * D * 2u;
+  static constexpr int kNumBars = 2 * kCrossStages + 2 * kCrossQBufs + 7;
+  static constexpr size_t bytes() {
+    return 1024 + (kCrossStages + kCrossQBufs) * kTile + kNumBars * 8 + 16;
+  }
+};
+
+// One item of work, the same for every role.
+struct CrossItem {
+  int bh, b, h, hk, tile, tiles, j0, T, nv, split;
+  __device__ __forceinline__ void at(const CrossFwdArgs& a, int i) {
+    split = i % a.splits;
+    const int p = i / a.splits;
+    bh = p / a.pairs;
+    tile = 2 * (p % a.pairs);
+    tiles = min(2, (a.Lq + 127) / 128 - tile);
+    b = bh / a.heads;
+    h = bh % a.heads;
+    hk = h / (a.heads / a.kv_heads);
+    nv = a.count == nullptr ? a.Lk : __ldg(a.count + b);
+    const int nt = (nv + 127) / 128;
+    j0 = nt * split / a.splits;
+    T = nt * (split + 1) / a.splits - j0;
+  }
+  // The first item from i on (in this CTA's stride) that has keys.
+  __device__ __forceinline__ bool with_keys(const CrossFwdArgs& a, int& i) {
+    for (; i < a.n_items; i += gridDim.x) {
+      at(a, i);
+      if (T > 0) return true;
+    }
+    return false;
+  }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kCrossFwdThreads, 1)
+cross_fwd_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                       const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CrossFwdArgs a) {
+  using namespace sm100;
+  using Lay = CrossFwdLayout<D>;
+  constexpr int CB = D / 64, NS = kCrossStages, NQ = kCrossQBufs;
+  constexpr uint32_t TILE = Lay::kTile, OC = 256;
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sQ = smem;
+  uint8_t* sRing = smem + NQ * TILE;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sRing + NS * TILE);
+  uint64_t* empty = full + NS;
+  uint64_t* q_full = empty + NS;
+  uint64_t* q_empty = q_full + NQ;
+  uint64_t* s_full = q_empty + NQ;  // [2]
+  uint64_t* p_full = s_full + 2;    // [2]
+  uint64_t* o_full = p_full + 2;    // [2]
+  uint64_t* mma_idle = o_full + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(full + Lay::kNumBars);
+  volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < NQ; ++s) {
+      mbar_init(&q_full[s], 1);
+      mbar_init(&q_empty[s], 1);
+    }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&s_full[x], 1);
+      mbar_init(&p_full[x], 128);
+      mbar_init(&o_full[x], 1);
+    }
+    mbar_init(mma_idle, 1);
+    *abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+
+  // Registers: 2 x 128 x 200 + 128 x 104 = 384 x 168, the launch total.
+  if (warp >= 8) {
+   asm volatile("setmaxnreg.dec.sync.aligned.u32 104;\n" ::: "memory");
+   if (warp == 8) {
+    // ================================================================ producer
+    if (lane == 0) {
+      prefetch_tensormap(&tmQ);
+      prefetch_tensormap(&tmK);
+      prefetch_tensormap(&tmV);
+      int it = 0, nq = 0;  // ring items and Q tiles loaded
+      bool ok = true;
+      const bool packed = a.count != nullptr;
+      auto load = [&](const CUtensorMap* map, const CrossItem& w, int j) {
+        const int s = it % NS;
+        if (!(ok = ok && mbar_wait(&empty[s], ((it / NS) & 1) ^ 1, abort))) return;
+        mbar_expect_tx(&full[s], TILE);
+        const int kh = w.bh / a.heads * a.kv_heads + w.hk;
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb)
+          tma_load_4d(sRing + s * TILE + cb * 128 * 128, map, &full[s], cb * 64, (w.j0 + j) * 128,
+                      packed ? kh : w.hk, packed ? 0 : w.b);
+        ++it;
+      };
+      auto load_q = [&](const CrossItem& w, int x) {
+        const int s = nq % NQ;
+        if (!(ok = ok && mbar_wait(&q_empty[s], ((nq / NQ) & 1) ^ 1, abort))) return;
+        mbar_expect_tx(&q_full[s], TILE);
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb)
+          tma_load_4d(sQ + s * TILE + cb * 128 * 128, &tmQ, &q_full[s], cb * 64, (w.tile + x) * 128, w.h, w.b);
+        ++nq;
+      };
+      CrossItem cur, nxt;
+      int i = blockIdx.x;
+      bool has = cur.with_keys(a, i);
+      if (has) {
+        load_q(cur, 0);
+        load(&tmK, cur, 0);
+        if (cur.tiles > 1) load_q(cur, 1);
+      }
+      while (ok && has) {
+        i += gridDim.x;
+        const bool more = nxt.with_keys(a, i);
+        for (int u = 0; ok && u < cur.T; ++u) {
+          const bool last = u + 1 == cur.T;
+          if (last && more) load_q(nxt, 0);
+          load(&tmV, cur, u);
+          if (!last) {
+            load(&tmK, cur, u + 1);
+          } else if (more) {
+            load(&tmK, nxt, 0);
+            if (nxt.tiles > 1) load_q(nxt, 1);
+          }
+        }
+        cur = nxt;
+        has = more;
+      }
+      // the copies already issued land before the CTA can exit
+      for (int u = it > NS ? it - NS : 0; u < it; ++u) mbar_drain(&full[u % NS], (u / NS) & 1);
+      for (int u = nq > NQ ? nq - NQ : 0; u < nq; ++u) mbar_drain(&q_full[u % NQ], (u / NQ) & 1);
+    }
+    __syncwarp();
+   } else if (warp == 9) {
+    // ================================================================ MMA issuer
+    // The whole warp runs the loop (warp-uniform operands); one elected lane
+    // issues each tcgen05 instruction.
+    constexpr uint32_t idS = idesc_bf16(128, 128, false, false);
+    constexpr uint32_t idO = idesc_bf16(128, D, false, true);
+    const uint32_t ring = smem_u32(sRing), qbase = smem_u32(sQ);
+    int it = 0, steps[2] = {0, 0};
+    bool ok = true;
+    auto take = [&](int& s) {
+      s = it % NS;
+      if (!(ok = ok && mbar_wait(&full[s], (it / NS) & 1, abort))) return;
+      fence_after_sync();
+      ++it;
+    };
+    auto wait_q = [&](int n) {
+      if (!(ok = ok && mbar_wait(&q_full[n % NQ], (n / NQ) & 1, abort))) return;
+      fence_after_sync();
+    };
+    // S_x = Q K^T with Q tile number n; `done`: the tile's last one
+    auto s_mmas = [&](int x, int n, int ks, bool done) {
+      const uint32_t qb = qbase + (n % NQ) * TILE, kb = ring + ks * TILE;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t off = (kk >> 2) * 128 * 128 + (kk & 3) * 32;
+        mma_ss_warp(tmem + x * 128, desc_sw128(qb + off, 16, 1024), desc_sw128(kb + off, 16, 1024), idS,
+                    kk > 0 ? 1u : 0u);
+      }
+      mma_commit_warp(&s_full[x]);
+      if (done) mma_commit_warp(&q_empty[n % NQ]);
+    };
+    CrossItem cur, nxt;
+    int i = blockIdx.x, nq = 0, ks = 0, vs = 0;
+    bool has = cur.with_keys(a, i);
+    if (has) {
+      take(ks);
+      for (int x = 0; ok && x < cur.tiles; ++x) {
+        wait_q(x);
+        if (ok) s_mmas(x, x, ks, cur.T == 1);
+      }
+      if (ok) mma_commit_warp(&empty[ks]);
+    }
+    while (ok && has) {
+      i += gridDim.x;
+      const bool more = nxt.with_keys(a, i);
+      const int nq2 = nq + cur.tiles;
+      for (int u = 0; ok && u < cur.T; ++u) {
+        const bool last = u + 1 == cur.T;
+        const bool next = !last || more;  // S tiles follow
+        take(vs);
+        if (ok && next) take(ks);
+        for (int x = 0; ok && x < 2; ++x) {
+          if (x < cur.tiles) {
+            if (!(ok = mbar_wait(&p_full[x], steps[x] & 1, abort))) break;
+            ++steps[x];
+            fence_after_sync();
+            const uint32_t vb = ring + vs * TILE;
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              mma_ts_warp(tmem + OC + x * D, tmem + x * 128 + kk * 8, desc_sw128(vb + kk * 16 * 128, 128 * 128, 1024),
+                          idO, (u > 0 || kk > 0) ? 1u : 0u);
+            if (last) mma_commit_warp(&o_full[x]);
+          }
+          if (!last) {
+            if (x < cur.tiles) s_mmas(x, nq + x, ks, u + 2 == cur.T);
+          } else if (more && x < nxt.tiles) {
+            wait_q(nq2 + x);
+            if (ok) s_mmas(x, nq2 + x, ks, nxt.T == 1);
+          }
+        }
+        if (!ok) break;
+        mma_commit_warp(&empty[vs]);
+        if (next) mma_commit_warp(&empty[ks]);
+      }
+      cur = nxt;
+      nq = nq2;
+      has = more;
+    }
+    // every MMA issued completes before TMEM is freed
+    mma_commit_warp(mma_idle);
+    mbar_drain(mma_idle, 0);
+    __syncwarp();
+   }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;\n" ::: "memory");
+    // ================================================================ softmax: tile A (warps 0-3), B (4-7)
+    const int x = warp / 4, row = threadIdx.x % 128;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp % 4) * 32) << 16);
+    const uint32_t sbase = lane_base + x * 128, obase = lane_base + OC + x * D;
+    const float c2 = a.scale_log2;
+    int steps = 0, outs = 0;
+    bool ok = true;
+    CrossItem w;
+    for (int i = blockIdx.x; ok && i < a.n_items; i += gridDim.x) {
+      w.at(a, i);
+      if (x >= w.tiles) continue;
+      float m = -INFINITY, l = 0.f;
+      uint32_t s[128];
+      for (int u = 0; u < w.T; ++u) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&s_full[x], steps & 1, abort))) {
+          ok = false;
+          break;
+        }
+        ++steps;
+        fence_after_sync();
+        tmem_ld32(sbase, s);
+        tmem_ld32(sbase + 32, s + 32);
+        tmem_ld32(sbase + 64, s + 64);
+        tmem_ld32(sbase + 96, s + 96);
+        tmem_wait_ld();
+        const int valid = w.nv - (w.j0 + u) * 128;
+        if (valid < 128) {
+#pragma unroll
+          for (int c = 0; c < 128; ++c) s[c] = c < valid ? s[c] : 0xff800000u;
+        }
+        float t0 = -INFINITY, t1 = -INFINITY, t2 = -INFINITY, t3 = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 128; c += 8) {
+          t0 = fmax3(t0, __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+          t1 = fmax3(t1, __uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
+          t2 = fmax3(t2, __uint_as_float(s[c + 4]), __uint_as_float(s[c + 5]));
+          t3 = fmax3(t3, __uint_as_float(s[c + 6]), __uint_as_float(s[c + 7]));
+        }
+        // running maximum in binary units; O and l are rescaled only when it
+        // grows by more than 8 (exact: both carry the same factor)
+        const float m_new = fmaxf(m, fmax3(fmaxf(t0, t1), t2, t3) * c2);
+        float f = 1.f;
+        if (m_new > m + 8.f) {
+          if (m != -INFINITY) {
+            f = ex2(m - m_new);
+            l *= f;
+          }
+          m = m_new;
+        }
+        // O is quiescent: this S was issued after the tile's last P V
+        if (__any_sync(0xffffffffu, f != 1.f)) {
+          uint32_t o[32];
+#pragma unroll 1
+          for (int ch = 0; ch < D / 32; ++ch) {
+            tmem_ld32(obase + ch * 32, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tmem_st32(obase + ch * 32, o);
+          }
+          tmem_wait_st();
+        }
+        const float mu = m == -INFINITY ? 0.f : m;
+        const uint64_t c2x2 = f2_pack(c2, c2), nmu = f2_pack(-mu, -mu);
+        uint64_t acc = 0;
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+#pragma unroll
+          for (int c = hh * 64; c < hh * 64 + 64; c += 2) {
+            const uint64_t t = ffma2(f2_pack(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), c2x2, nmu);
+            const float p0 = ex2(f2_lo(t)), p1 = ex2(f2_hi(t));
+            acc = fadd2(acc, f2_pack(p0, p1));
+            s[c >> 1] = pack_bf16x2(p0, p1);  // the product's operand type; the sum keeps 32 bits
+          }
+          if (hh == 0) tmem_st32(sbase, s);
+        }
+        l += f2_lo(acc) + f2_hi(acc);
+        tmem_st32(sbase + 32, s + 32);
+        tmem_wait_st();
+        fence_before_sync();
+        mbar_arrive(&p_full[x]);
+      }
+      if (!ok) break;
+      // epilogue: o = O / l (0 without keys)
+      if (w.T > 0) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&o_full[x], outs & 1, abort))) {
+          ok = false;
+          break;
+        }
+        ++outs;
+        fence_after_sync();
+      }
+      const int qrow = (w.tile + x) * 128 + row;
+      const bool in = qrow < a.Lq;
+      const float inv = w.T > 0 ? 1.f / l : 0.f;
+      const float lse2 = w.T > 0 ? m + log2f(l) : -INFINITY;
+      const int64_t flat = (int64_t)w.bh * a.Lq + qrow;
+      if (a.splits > 1) {
+        const int64_t at = (int64_t)w.split * a.BH * a.Lq + flat;
+        if (in) a.part_lse[at] = lse2;
+        if (w.T == 0) continue;  // weight zero: the share's output is not read
+#pragma unroll 1
+        for (int ch = 0; ch < D / 32; ++ch) {
+          uint32_t o[32];
+          tmem_ld32(obase + ch * 32, o);
+          tmem_wait_ld();
+          if (in) {
+            float4* dst = reinterpret_cast<float4*>(a.part + at * D + ch * 32);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              dst[e] = make_float4(__uint_as_float(o[4 * e]) * inv, __uint_as_float(o[4 * e + 1]) * inv,
+                                   __uint_as_float(o[4 * e + 2]) * inv, __uint_as_float(o[4 * e + 3]) * inv);
+          }
+        }
+      } else {
+        if (in && a.lse != nullptr) a.lse[flat] = lse2 * 0.6931471805599453f;
+        __nv_bfloat16* dst = a.out + w.b * a.so.b + w.h * a.so.h + (int64_t)qrow * a.so.r;
+#pragma unroll 1
+        for (int ch = 0; ch < D / 32; ++ch) {
+          uint32_t o[32], pk[16];
+          if (w.T > 0) {
+            tmem_ld32(obase + ch * 32, o);
+            tmem_wait_ld();
+          }
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            pk[e] = w.T > 0 ? pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv) : 0u;
+          if (in) {
+            uint4* d4 = reinterpret_cast<uint4*>(dst + ch * 32);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) d4[e] = make_uint4(pk[4 * e], pk[4 * e + 1], pk[4 * e + 2], pk[4 * e + 3]);
+          }
+        }
+      }
+      fence_before_sync();  // before this tile's next P releases the P V that overwrites O
+    }
+  }
+
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  if (warp == 9) tmem_dealloc(tmem, 512);
+}
+
+// Joins the shares: out = sum_s w_s o_s / sum_s w_s with w_s = 2^(lse_s - max).
+// D / 4 threads per row.
+template <int D>
+__global__ void __launch_bounds__(256) cross_join_kernel(const CrossFwdArgs a) {
+  const int64_t rows = (int64_t)a.BH * a.Lq;
+  const int64_t flat = (int64_t)blockIdx.x * (256 / (D / 4)) + threadIdx.x / (D / 4);
+  if (flat >= rows) return;
+  const int c = threadIdx.x % (D / 4) * 4;
+  float top = -INFINITY;
+  for (int s = 0; s < a.splits; ++s) top = fmaxf(top, a.part_lse[s * rows + flat]);
+  float sum = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s = 0; s < a.splits; ++s) {
+    const float z = a.part_lse[s * rows + flat];
+    if (z == -INFINITY) continue;
+    const float w = exp2f(z - top);
+    const float4 y = *reinterpret_cast<const float4*>(a.part + (s * rows + flat) * D + c);
+    sum += w;
+    o.x += w * y.x;
+    o.y += w * y.y;
+    o.z += w * y.z;
+    o.w += w * y.w;
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const int bh = (int)(flat / a.Lq), b = bh / a.heads, h = bh % a.heads;
+  put4(a.out + b * a.so.b + h * a.so.h + (flat % a.Lq) * a.so.r + c, o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+  if (a.lse != nullptr && c == 0)
+    a.lse[flat] = top == -INFINITY ? top : (top + log2f(sum)) * 0.6931471805599453f;
+}
+
+}  // namespace pisa

@@ -179,7 +179,7 @@ CrossPackPlan cross_pack_plan(const CrossShape& s, bool backward) {
 
 struct CrossFwdPlan {
   CrossPackPlan pack;
-  int pairs, splits;
+  int splits;
   size_t part, part_lse, total;
 };
 
@@ -191,8 +191,7 @@ CrossFwdPlan cross_fwd_plan(const CrossShape& s) {
   p.splits = 1;
   if (s.dtype == PISA_BF16) {
     p.pack = cross_pack_plan(s, false);
-    p.pairs = ((s.Lq + 127) / 128 + 1) / 2;
-    const long long items = (long long)s.batch * s.heads * p.pairs, tiles = (s.Lk + 127) / 128;
+    const long long items = (long long)s.batch * s.heads * (((s.Lq + 127) / 128 + 1) / 2), tiles = (s.Lk + 127) / 128;
     if (2 * items <= kSMs && tiles > 1) p.splits = (int)(kSMs / items < tiles ? kSMs / items : tiles);
     if (p.splits > 1) {
       const size_t rows = (size_t)p.splits * s.batch * s.heads * s.Lq;
@@ -206,24 +205,34 @@ CrossFwdPlan cross_fwd_plan(const CrossShape& s) {
 }
 
 struct CrossBwdPlan {
-  int splits;
+  CrossPackPlan pack;
+  int splits;  // CUDA cores: shares of the query tiles; tensor cores: CTAs of the dk/dv kernel
   size_t delta, part, total;
 };
 
-// Query shares per key tile: enough CTAs for two per SM, at least eight query
-// tiles each, and partials of at most 256 MB.
+// fp32: query shares per key tile, enough CTAs for two per SM, at least eight
+// query tiles each, and partials of at most 256 MB.  bf16: one CTA per SM, but
+// at least eight steps of 64 query rows each.
 CrossBwdPlan cross_bwd_plan(const CrossShape& s) {
   CrossBwdPlan p{};
-  const long long ctas = (long long)s.batch * s.kv_heads * ((s.Lk + 63) / 64);
-  const long long tiles = (long long)(s.heads / s.kv_heads) * ((s.Lq + 31) / 32);
-  const long long one = 2LL * s.batch * s.kv_heads * s.Lk * s.d * sizeof(float);
-  long long n = (2LL * kSMs + ctas - 1) / ctas;
-  if (n > tiles / 8) n = tiles / 8;
-  if (n > (256LL << 20) / one) n = (256LL << 20) / one;
-  p.splits = (int)(n < 1 ? 1 : n);
+  const long long group = s.heads / s.kv_heads, slices = (long long)s.batch * s.kv_heads;
   p.delta = align_up((size_t)s.batch * s.heads * s.Lq * sizeof(float));
-  p.part = p.splits > 1 ? align_up((size_t)p.splits * one) : 0;
-  p.total = p.delta + p.part;
+  if (s.dtype == PISA_BF16) {
+    p.pack = cross_pack_plan(s, true);
+    const long long items = slices * ((s.Lk + 127) / 128), steps = items * group * ((s.Lq + 63) / 64);
+    const long long n = (steps + 7) / 8;
+    p.splits = (int)(n < kSMs ? n : kSMs);
+    p.part = align_up((size_t)(items + p.splits) * 2 * 128 * s.d * sizeof(float));
+  } else {
+    const long long ctas = slices * ((s.Lk + 63) / 64), tiles = group * ((s.Lq + 31) / 32);
+    const long long one = 2LL * slices * s.Lk * s.d * sizeof(float);
+    long long n = (2LL * kSMs + ctas - 1) / ctas;
+    if (n > tiles / 8) n = tiles / 8;
+    if (n > (256LL << 20) / one) n = (256LL << 20) / one;
+    p.splits = (int)(n < 1 ? 1 : n);
+    p.part = p.splits > 1 ? align_up((size_t)p.splits * one) : 0;
+  }
+  p.total = p.pack.total + p.delta + p.part;
   return p;
 }
 
@@ -253,17 +262,26 @@ CrossArgs cross_args(const CrossShape& s, const int32_t* kv_len, const uint8_t* 
   return a;
 }
 
-// Packs the allowed keys (bf16): fills the maps, the count and, for the
-// backward pass, the places; without a mask the maps are those of k and v.
+// Keys and values as the tensor-core kernels read them: the caller's, or the
+// packed copies with their counts and, for the backward pass, places.
+struct CrossKeys {
+  const void *k, *v;
+  HeadView sk, sv;
+  int rows, heads, batch;  // extents of the maps
+  const int32_t *count, *place;
+};
+
 template <int D>
-pisa_status run_cross_pack(const CrossArgs& a, const CrossShape& s, const CrossPackPlan& p, char* ws, CUtensorMap* mK,
-                           CUtensorMap* mV, const int32_t** count, const int32_t** place, cudaStream_t st) {
-  *count = *place = nullptr;
-  if (!s.masked)
-    return make_map_view(mK, a.k, D, s.Lk, s.kv_heads, s.batch, a.sk) &&
-                   make_map_view(mV, a.v, D, s.Lk, s.kv_heads, s.batch, a.sv)
-               ? PISA_OK
-               : PISA_ERR_CUDA;
+bool cross_key_maps(const CrossKeys& x, uint32_t box_rows, CUtensorMap* mK, CUtensorMap* mV) {
+  return make_map_view(mK, x.k, D, x.rows, x.heads, x.batch, x.sk, box_rows) &&
+         make_map_view(mV, x.v, D, x.rows, x.heads, x.batch, x.sv, box_rows);
+}
+
+template <int D>
+pisa_status run_cross_pack(const CrossArgs& a, const CrossShape& s, const CrossPackPlan& p, char* ws, CrossKeys* x,
+                           cudaStream_t st) {
+  *x = CrossKeys{a.k, a.v, a.sk, a.sv, s.Lk, s.kv_heads, s.batch, nullptr, nullptr};
+  if (!s.masked) return PISA_OK;
   CrossPackArgs c{};
   c.k = a.k;
   c.v = a.v;
@@ -278,13 +296,10 @@ pisa_status run_cross_pack(const CrossArgs& a, const CrossShape& s, const CrossP
   c.kv_heads = s.kv_heads;
   c.Lk = s.Lk;
   c.padded = p.padded;
-  const uint64_t slices = (uint64_t)s.batch * s.kv_heads;
+  const int slices = s.batch * s.kv_heads;
   const HeadView dense{(int64_t)slices * p.padded * D, (int64_t)p.padded * D, D};
-  if (!make_map_view(mK, c.pk, D, p.padded, slices, 1, dense) || !make_map_view(mV, c.pv, D, p.padded, slices, 1, dense))
-    return PISA_ERR_CUDA;
-  cross_pack_kernel<D><<<dim3(p.padded / kPackRows, (unsigned)slices), kPackThreads, 0, st>>>(c);
-  *count = c.count;
-  *place = c.place;
+  *x = CrossKeys{c.pk, c.pv, dense, dense, p.padded, slices, 1, c.count, c.place};
+  cross_pack_kernel<D><<<dim3(p.padded / kPackRows, slices), kPackThreads, 0, st>>>(c);
   return last_launch();
 }
 
@@ -294,29 +309,36 @@ bool sm_count(int* sms) {
          cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess;
 }
 
-template <int D>
-pisa_status run_cross_fwd_sm100(const CrossArgs& a, const CrossShape& s, char* ws, cudaStream_t st) {
-  const CrossFwdPlan p = cross_fwd_plan(s);
-  CUtensorMap mQ, mK, mV;
-  const int32_t *count, *place;
-  if (pisa_status e = run_cross_pack<D>(a, s, p.pack, ws, &mK, &mV, &count, &place, st)) return e;
-  if (!make_map_view(&mQ, a.q, D, s.Lq, s.heads, s.batch, a.sq)) return PISA_ERR_CUDA;
+// The items of a kernel that walks pairs of query tiles.
+CrossFwdArgs cross_work(const CrossShape& s, const int32_t* count, int splits) {
   CrossFwdArgs f{};
-  f.out = static_cast<__nv_bfloat16*>(a.out);
-  f.so = a.so;
-  f.lse = a.lse;
   f.count = count;
-  f.part = reinterpret_cast<float*>(ws + p.pack.total);
-  f.part_lse = reinterpret_cast<float*>(ws + p.pack.total + p.part);
   f.heads = s.heads;
   f.kv_heads = s.kv_heads;
   f.Lq = s.Lq;
   f.Lk = s.Lk;
   f.BH = s.batch * s.heads;
-  f.pairs = p.pairs;
-  f.splits = p.splits;
-  f.n_items = f.BH * p.pairs * p.splits;
-  f.scale_log2 = kLog2e * a.scale;
+  f.pairs = ((s.Lq + 127) / 128 + 1) / 2;
+  f.splits = splits;
+  f.n_items = f.BH * f.pairs * splits;
+  f.scale_log2 = kLog2e / sqrtf((float)s.d);
+  return f;
+}
+
+template <int D>
+pisa_status run_cross_fwd_sm100(const CrossArgs& a, const CrossShape& s, char* ws, cudaStream_t st) {
+  const CrossFwdPlan p = cross_fwd_plan(s);
+  CUtensorMap mQ, mK, mV;
+  CrossKeys x;
+  if (pisa_status e = run_cross_pack<D>(a, s, p.pack, ws, &x, st)) return e;
+  if (!make_map_view(&mQ, a.q, D, s.Lq, s.heads, s.batch, a.sq, 128) || !cross_key_maps<D>(x, 128, &mK, &mV))
+    return PISA_ERR_CUDA;
+  CrossFwdArgs f = cross_work(s, x.count, p.splits);
+  f.out = static_cast<__nv_bfloat16*>(a.out);
+  f.so = a.so;
+  f.lse = a.lse;
+  f.part = reinterpret_cast<float*>(ws + p.pack.total);
+  f.part_lse = reinterpret_cast<float*>(ws + p.pack.total + p.part);
   int sms = 0;
   if (!sm_count(&sms)) return PISA_ERR_CUDA;
   const size_t smem = CrossFwdLayout<D>::bytes();
@@ -344,19 +366,79 @@ struct CrossFwdOp {
   }
 };
 
+template <int D>
+pisa_status run_cross_bwd_sm100(const CrossArgs& a, const CrossShape& s, char* ws, cudaStream_t st) {
+  const CrossBwdPlan p = cross_bwd_plan(s);
+  CrossKeys x;
+  if (pisa_status e = run_cross_pack<D>(a, s, p.pack, ws, &x, st)) return e;
+  CUtensorMap q128, g128, q64, g64, k64, v64, k128, v128;
+  if (!make_map_view(&q128, a.q, D, s.Lq, s.heads, s.batch, a.sq, 128) ||
+      !make_map_view(&g128, a.g, D, s.Lq, s.heads, s.batch, a.sg, 128) ||
+      !make_map_view(&q64, a.q, D, s.Lq, s.heads, s.batch, a.sq, 64) ||
+      !make_map_view(&g64, a.g, D, s.Lq, s.heads, s.batch, a.sg, 64) || !cross_key_maps<D>(x, 64, &k64, &v64) ||
+      !cross_key_maps<D>(x, 128, &k128, &v128))
+    return PISA_ERR_CUDA;
+  CrossDqArgs f{};
+  f.dq = static_cast<__nv_bfloat16*>(a.dq);
+  f.g = static_cast<const __nv_bfloat16*>(a.g);
+  f.o = static_cast<const __nv_bfloat16*>(a.o);
+  f.sdq = a.sdq;
+  f.sg = a.sg;
+  f.so = a.so;
+  f.lse = a.lse;
+  f.delta = reinterpret_cast<float*>(ws + p.pack.total);
+  f.w = cross_work(s, x.count, 1);
+  f.scale = a.scale;
+  int sms = 0;
+  if (!sm_count(&sms)) return PISA_ERR_CUDA;
+  const size_t s1 = CrossDqLayout<D>::bytes(), s2 = CrossDkvLayout<D>::bytes();
+  if (!set_smem(cross_dq_sm100_kernel<D>, s1) || !set_smem(cross_dkv_sm100_kernel<D>, s2)) return PISA_ERR_CUDA;
+  cross_dq_sm100_kernel<D><<<f.w.n_items < sms ? f.w.n_items : sms, kCrossBwdThreads, s1, st>>>(q128, g128, k64, v64, f);
+  if (last_launch() != PISA_OK) return PISA_ERR_CUDA;
+  CrossReduceArgs r{};
+  r.a = CrossDkvArgs{a.lse, f.delta, x.count, reinterpret_cast<float*>(ws + p.pack.total + p.delta),
+                     s.batch, s.heads, s.kv_heads, s.Lq, s.Lk, f.w.scale_log2};
+  r.place = x.place;
+  r.dk = static_cast<__nv_bfloat16*>(a.dk);
+  r.dv = static_cast<__nv_bfloat16*>(a.dv);
+  r.sdk = a.sdk;
+  r.sdv = a.sdv;
+  r.scale = a.scale;
+  r.ctas = p.splits;
+  cross_dkv_sm100_kernel<D><<<p.splits, kCrossBwdThreads, s2, st>>>(q64, g64, k128, v128, r.a);
+  if (last_launch() != PISA_OK) return PISA_ERR_CUDA;
+  constexpr int rows = 256 / (D / 4);
+  const long long n = ((long long)s.batch * s.kv_heads * s.Lk + rows - 1) / rows;
+  cross_dkv_reduce_kernel<D><<<dim3((unsigned)n, 2), 256, 0, st>>>(r);
+  return last_launch();
+}
+
+template <int D>
+pisa_status run_cross_bwd_simt(CrossArgs a, const CrossShape& s, char* ws, cudaStream_t st) {
+  const CrossBwdPlan p = cross_bwd_plan(s);
+  a.splits = p.splits;
+  a.delta = reinterpret_cast<float*>(ws);
+  a.part = reinterpret_cast<float*>(ws + p.delta);
+  const size_t s1 = CrossBwdSimt<D>::dq_bytes(), s2 = CrossBwdSimt<D>::dkv_bytes();
+  if (!set_smem(cross_dq_simt_kernel<float, D>, s1) || !set_smem(cross_dkv_simt_kernel<float, D>, s2))
+    return PISA_ERR_CUDA;
+  cross_dq_simt_kernel<float, D><<<dim3((s.Lq + 63) / 64, s.batch * s.heads), kCrossThreads, s1, st>>>(a);
+  if (last_launch() != PISA_OK) return PISA_ERR_CUDA;
+  cross_dkv_simt_kernel<float, D>
+      <<<dim3((s.Lk + 63) / 64, s.batch * s.kv_heads, a.splits), kCrossThreads, s2, st>>>(a);
+  if (last_launch() != PISA_OK || a.splits == 1) return last_launch();
+  const long long n = (long long)s.batch * s.kv_heads * s.Lk * D / 4;
+  cross_dkv_sum_kernel<float, D><<<dim3((unsigned)((n + 255) / 256), 2), 256, 0, st>>>(a);
+  return last_launch();
+}
+
 template <typename T, int D>
 struct CrossBwdOp {
-  static pisa_status run(const CrossArgs& a, const CrossShape& s, cudaStream_t st) {
-    const size_t s1 = CrossBwdSimt<D>::dq_bytes(), s2 = CrossBwdSimt<D>::dkv_bytes();
-    if (!set_smem(cross_dq_simt_kernel<T, D>, s1) || !set_smem(cross_dkv_simt_kernel<T, D>, s2)) return PISA_ERR_CUDA;
-    cross_dq_simt_kernel<T, D><<<dim3((s.Lq + 63) / 64, s.batch * s.heads), kCrossThreads, s1, st>>>(a);
-    if (last_launch() != PISA_OK) return PISA_ERR_CUDA;
-    cross_dkv_simt_kernel<T, D>
-        <<<dim3((s.Lk + 63) / 64, s.batch * s.kv_heads, a.splits), kCrossThreads, s2, st>>>(a);
-    if (last_launch() != PISA_OK || a.splits == 1) return last_launch();
-    const long long n = (long long)s.batch * s.kv_heads * s.Lk * D / 4;
-    cross_dkv_sum_kernel<T, D><<<dim3((unsigned)((n + 255) / 256), 2), 256, 0, st>>>(a);
-    return last_launch();
+  static pisa_status run(const CrossArgs& a, const CrossShape& s, char* ws, cudaStream_t st) {
+    if constexpr (std::is_same<T, __nv_bfloat16>::value)
+      return run_cross_bwd_sm100<D>(a, s, ws, st);
+    else
+      return run_cross_bwd_simt<D>(a, s, ws, st);
   }
 };
 
@@ -393,8 +475,7 @@ pisa_status cross_bwd_api(const void* dout, const void* q, const void* k, const 
   HeadView w[8];
   if (!cross_tensors_ok(s, ptr, "qqkkqqkk", 8, strides, w)) return PISA_ERR_INVALID_ARG;
   if (lse == nullptr || !aligned_to(lse, 4) || !aligned_to(kv_len, 4)) return PISA_ERR_INVALID_ARG;
-  const CrossBwdPlan p = cross_bwd_plan(s);
-  if (ws == nullptr || ws_bytes < p.total) return PISA_ERR_WORKSPACE;
+  if (ws == nullptr || ws_bytes < cross_bwd_plan(s).total) return PISA_ERR_WORKSPACE;
   if (!aligned16(ws)) return PISA_ERR_INVALID_ARG;
   CrossArgs a = cross_args(s, kv_len, key_mask);
   a.g = dout;
@@ -414,11 +495,8 @@ pisa_status cross_bwd_api(const void* dout, const void* q, const void* k, const 
   a.sdq = w[5];
   a.sdk = w[6];
   a.sdv = w[7];
-  a.splits = p.splits;
-  a.delta = reinterpret_cast<float*>(ws);
-  a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + p.delta);
   NvtxRange range("pisa.cross_bwd");
-  return dispatch<CrossBwdOp>(s.dtype, s.d, a, s, st);
+  return dispatch<CrossBwdOp>(s.dtype, s.d, a, s, static_cast<char*>(ws), st);
 }
 
 }  // namespace

@@ -1,0 +1,810 @@
+// Gradients of the cross-attention on the 5th-generation tensor cores (bf16
+// inputs): one kernel for dq (and delta), one for dk and dv.
+//
+// The scores and dp are formed twice, once with the queries and once with the
+// keys as accumulator rows: 7 products of Lq x Lk x d instead of 5.  In return
+// each gradient is summed in TMEM by the CTA that owns its rows: no atomics, no
+// 32-bit dq in memory, bit-reproducible.  p and ds enter their products in
+// bf16 (the operand type of the MMA; their sums are 32-bit).
+#pragma once
+
+#include "cross_sm100.cuh"
+
+namespace pisa {
+
+__device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// ------------------------------------------------------------------ dq
+//
+// Items: pairs of 128-row query tiles (A, B) of one head, key steps of 64.
+//   S_x = Q_x K^T, dP_x = G_x V^T;  P = 2^(c S - lse2),  dS = P (dP - delta) -> bf16
+//   over S_x in TMEM;  dQ_x += dS_x K;  at the end dq = s dQ.
+// TMEM at d = 128 is full with S, dP (64 columns each) and dQ of both tiles,
+// which is why a step has 64 keys: an MMA with N = 64 takes 53 cycles, one with
+// N = 128 takes 64, but two tiles in turn keep the tensor pipe busy while each
+// one's exponentials run.  TMEM columns: [128x, +64) S_x, [128x + 64, +64) dP_x,
+// [256 + x D, +D) dQ_x.
+//
+// Warps 0-3 / 4-7: rows of tile A / B, 8: TMA producer, 9: MMA issuer, 10 / 11:
+// delta of tile A / B, one item ahead (delta_i = g_i . o_i, coalesced reads of
+// both, into shared memory and to global memory for the dk/dv kernel).  With a
+// single step of keys delta is instead sum_j p_ij dp_ij, formed in 32 bits from
+// what the row holds: with few keys ds is a small difference of dp and delta,
+// and the rounding of the stored bf16 output would dominate it (two keys:
+// error 1.7x that of the final rounding; 64 keys: 1 part in 24 of the variance).
+struct CrossDqArgs {
+  __nv_bfloat16* dq;
+  const __nv_bfloat16 *g, *o;
+  HeadView sdq, sg, so;
+  const float* lse;
+  float* delta;
+  CrossFwdArgs w;  // shape of the work: heads, kv_heads, Lq, Lk, pairs, count (splits = 1)
+  float scale;
+};
+
+constexpr int kCrossBwdThreads = 384, kDqStages = 5;
+
+template <int D>
+struct CrossDqLayout {
+  static constexpr uint32_t kRows = 128u * D * 2u;  // one of Q, G of a tile
+  static constexpr uint32_t kSlot = 64u * D * 2u;   // one of K, V of a step
+  static constexpr int kNumBars = 2 * kDqStages + 2 + 2 + 2 + 2 + 2 + 4 + 4 + 1;
+  static constexpr size_t bytes() {
+    return 1024 + 4 * kRows + kDqStages * kSlot + kNumBars * 8 + 16 + 4 * 128 * 8;
+  }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kCrossBwdThreads, 1)
+cross_dq_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmG,
+                      const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                      const __grid_constant__ CrossDqArgs a) {
+  using namespace sm100;
+  using Lay = CrossDqLayout<D>;
+  constexpr int CB = D / 64, NS = kDqStages;
+  constexpr uint32_t ROWS = Lay::kRows, SLOT = Lay::kSlot, OC = 256;
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sRows = smem;  // Q_A, G_A, Q_B, G_B
+  uint8_t* sRing = smem + 4 * ROWS;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sRing + NS * SLOT);
+  uint64_t* empty = full + NS;
+  uint64_t* q_full = empty + NS;     // [2]
+  uint64_t* q_empty = q_full + 2;    // [2]
+  uint64_t* s_full = q_empty + 2;    // [2]
+  uint64_t* p_full = s_full + 2;     // [2]
+  uint64_t* o_full = p_full + 2;     // [2]
+  uint64_t* d_full = o_full + 2;     // [2 tiles][2 buffers]
+  uint64_t* d_empty = d_full + 4;    // [2][2]
+  uint64_t* mma_idle = d_empty + 4;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(full + Lay::kNumBars);
+  volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  float2* rowv = reinterpret_cast<float2*>(tmem_slot + 4);  // [2 tiles][2 buffers][128]: (-lse2, -delta)
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&q_full[x], 1);
+      mbar_init(&q_empty[x], 1);
+      mbar_init(&s_full[x], 1);
+      mbar_init(&p_full[x], 128);
+      mbar_init(&o_full[x], 1);
+      for (int y = 0; y < 2; ++y) {
+        mbar_init(&d_full[2 * x + y], 32);
+        mbar_init(&d_empty[2 * x + y], 128);
+      }
+    }
+    mbar_init(mma_idle, 1);
+    *abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  const CrossFwdArgs& W = a.w;
+  const int n_items = W.n_items;
+  // An item's key steps of 64 (CrossItem counts tiles of 128).
+  auto key_steps = [](const CrossItem& w) { return (w.nv + 63) / 64; };
+
+  if (warp == 8) {
+    // ================================================================ producer
+    if (lane == 0) {
+      prefetch_tensormap(&tmQ);
+      prefetch_tensormap(&tmG);
+      prefetch_tensormap(&tmK);
+      prefetch_tensormap(&tmV);
+      int it = 0, nq[2] = {0, 0};
+      bool ok = true;
+      const bool packed = W.count != nullptr;
+      auto load = [&](const CUtensorMap* map, const CrossItem& w, int u) {
+        const int s = it % NS;
+        if (!(ok = ok && mbar_wait(&empty[s], ((it / NS) & 1) ^ 1, abort))) return;
+        mbar_expect_tx(&full[s], SLOT);
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb)
+          tma_load_4d(sRing + s * SLOT + cb * 64 * 128, map, &full[s], cb * 64, u * 64,
+                      packed ? w.b * W.kv_heads + w.hk : w.hk, packed ? 0 : w.b);
+        ++it;
+      };
+      auto load_rows = [&](const CrossItem& w) {
+        for (int x = 0; ok && x < w.tiles; ++x) {
+          if (!(ok = mbar_wait(&q_empty[x], (nq[x] & 1) ^ 1, abort))) return;
+          mbar_expect_tx(&q_full[x], 2 * ROWS);
+#pragma unroll
+          for (int cb = 0; cb < CB; ++cb) {
+            uint8_t* dst = sRows + 2 * x * ROWS + cb * 128 * 128;
+            tma_load_4d(dst, &tmQ, &q_full[x], cb * 64, (w.tile + x) * 128, w.h, w.b);
+            tma_load_4d(dst + ROWS, &tmG, &q_full[x], cb * 64, (w.tile + x) * 128, w.h, w.b);
+          }
+          ++nq[x];
+        }
+      };
+      CrossItem cur;
+      int i = blockIdx.x;
+      while (ok && cur.with_keys(W, i)) {
+        // the first keys of an item are loaded while the last item's queries
+        // are in use, its queries as their buffers become free
+        load(&tmK, cur, 0);
+        load(&tmV, cur, 0);
+        load_rows(cur);
+        for (int u = 1; ok && u < key_steps(cur); ++u) {
+          load(&tmK, cur, u);
+          load(&tmV, cur, u);
+        }
+        i += gridDim.x;
+      }
+      for (int u = it > NS ? it - NS : 0; u < it; ++u) mbar_drain(&full[u % NS], (u / NS) & 1);
+      for (int x = 0; x < 2; ++x)
+        if (nq[x] > 0) mbar_drain(&q_full[x], (nq[x] - 1) & 1);
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    // ================================================================ MMA issuer
+    constexpr uint32_t idS = idesc_bf16(128, 64, false, false);
+    constexpr uint32_t idO = idesc_bf16(128, D, false, true);
+    const uint32_t ring = smem_u32(sRing), rows = smem_u32(sRows);
+    int it = 0, steps[2] = {0, 0}, nq[2] = {0, 0};
+    bool ok = true;
+    auto take = [&](int& s) {
+      s = it % NS;
+      if (!(ok = ok && mbar_wait(&full[s], (it / NS) & 1, abort))) return;
+      fence_after_sync();
+      ++it;
+    };
+    // S_x and dP_x of one step; first / last: of the tile's item
+    auto s_mmas = [&](int x, int ks, int vs, bool first, bool last) {
+      if (first) {
+        if (!(ok = ok && mbar_wait(&q_full[x], nq[x] & 1, abort))) return;
+        ++nq[x];
+        fence_after_sync();
+      }
+      const uint32_t qb = rows + 2 * x * ROWS, kb = ring + ks * SLOT, vb = ring + vs * SLOT;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t ro = (kk >> 2) * 128 * 128 + (kk & 3) * 32, so = (kk >> 2) * 64 * 128 + (kk & 3) * 32;
+        mma_ss_warp(tmem + x * 128, desc_sw128(qb + ro, 16, 1024), desc_sw128(kb + so, 16, 1024), idS, kk > 0 ? 1u : 0u);
+      }
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t ro = (kk >> 2) * 128 * 128 + (kk & 3) * 32, so = (kk >> 2) * 64 * 128 + (kk & 3) * 32;
+        mma_ss_warp(tmem + x * 128 + 64, desc_sw128(qb + ROWS + ro, 16, 1024), desc_sw128(vb + so, 16, 1024), idS,
+                    kk > 0 ? 1u : 0u);
+      }
+      mma_commit_warp(&s_full[x]);
+      if (last) mma_commit_warp(&q_empty[x]);
+    };
+    CrossItem cur, nxt;
+    int i = blockIdx.x, ks = 0, vs = 0;
+    bool has = cur.with_keys(W, i);
+    if (has) {
+      take(ks);
+      take(vs);
+      for (int x = 0; ok && x < cur.tiles; ++x) s_mmas(x, ks, vs, true, key_steps(cur) == 1);
+      if (ok) mma_commit_warp(&empty[vs]);
+    }
+    while (ok && has) {
+      i += gridDim.x;
+      const bool more = nxt.with_keys(W, i);
+      const int T = key_steps(cur);
+      for (int u = 0; ok && u < T; ++u) {
+        const bool last = u + 1 == T, next = !last || more;
+        const int k0 = ks;
+        if (next) {
+          take(ks);
+          take(vs);
+        }
+        for (int x = 0; ok && x < 2; ++x) {
+          if (x < cur.tiles) {
+            if (!(ok = mbar_wait(&p_full[x], steps[x] & 1, abort))) break;
+            ++steps[x];
+            fence_after_sync();
+            const uint32_t kb = ring + k0 * SLOT;
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_ts_warp(tmem + OC + x * D, tmem + x * 128 + kk * 8, desc_sw128(kb + kk * 16 * 128, 64 * 128, 1024), idO,
+                          (u > 0 || kk > 0) ? 1u : 0u);
+            if (last) mma_commit_warp(&o_full[x]);
+          }
+          if (!last) {
+            if (x < cur.tiles) s_mmas(x, ks, vs, false, u + 2 == T);
+          } else if (more && x < nxt.tiles) {
+            s_mmas(x, ks, vs, true, key_steps(nxt) == 1);
+          }
+        }
+        if (!ok) break;
+        mma_commit_warp(&empty[k0]);
+        if (next) mma_commit_warp(&empty[vs]);
+      }
+      cur = nxt;
+      has = more;
+    }
+    mma_commit_warp(mma_idle);
+    mbar_drain(mma_idle, 0);
+    __syncwarp();
+  } else if (warp >= 10) {
+    // ================================================================ delta, one item ahead
+    const int x = warp - 10;
+    constexpr int LPR = D / 8, RPL = 32 / LPR;  // lanes per row, rows per load
+    int n = 0;
+    bool ok = true;
+    CrossItem w;
+    for (int i = blockIdx.x; ok && i < n_items; i += gridDim.x) {
+      w.at(W, i);
+      if (x >= w.tiles || w.T == 0) continue;
+      const int buf = n & 1;
+      if (!__all_sync(0xffffffffu, mbar_wait(&d_empty[2 * x + buf], ((n >> 1) & 1) ^ 1, abort))) {
+        ok = false;
+        break;
+      }
+      ++n;
+      float2* dst = rowv + (2 * x + buf) * 128;
+      const int row0 = (w.tile + x) * 128;
+      const int64_t flat = (int64_t)w.bh * W.Lq + row0;
+      const bool from_o = key_steps(w) > 1;
+      const __nv_bfloat16* g = a.g + w.b * a.sg.b + w.h * a.sg.h + (int64_t)row0 * a.sg.r + lane % LPR * 8;
+      const __nv_bfloat16* o = a.o + w.b * a.so.b + w.h * a.so.h + (int64_t)row0 * a.so.r + lane % LPR * 8;
+      for (int r0 = 0; r0 < 128; r0 += 32) {
+        float mine = 0.f;  // delta of row r0 + lane
+        if (from_o) {
+#pragma unroll 4
+          for (int k = 0; k < 32 / RPL; ++k) {
+            const int r = r0 + k * RPL + lane / LPR;
+            float t = 0.f;
+            if (row0 + r < W.Lq) {
+              float y[8], z[8];
+              load8(g + (int64_t)r * a.sg.r, y);
+              load8(o + (int64_t)r * a.so.r, z);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) t = fmaf(y[e], z[e], t);
+            }
+#pragma unroll
+            for (int s = LPR / 2; s > 0; s >>= 1) t += __shfl_xor_sync(0xffffffffu, t, s);
+            const float got = __shfl_sync(0xffffffffu, t, (lane % RPL) * LPR);
+            if (lane / RPL == k) mine = got;
+          }
+        }
+        const int r = r0 + lane;
+        float nl = -INFINITY;
+        if (row0 + r < W.Lq) {
+          nl = -a.lse[flat + r] * kLog2e;
+          if (from_o) a.delta[flat + r] = mine;
+        }
+        dst[r] = make_float2(nl, -mine);
+      }
+      mbar_arrive(&d_full[2 * x + buf]);
+    }
+  } else {
+    // ================================================================ rows of tile A (warps 0-3), B (4-7)
+    const int x = warp / 4, row = threadIdx.x % 128;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp % 4) * 32) << 16);
+    const uint32_t sbase = lane_base + x * 128, obase = lane_base + OC + x * D;
+    const float c2 = W.scale_log2;
+    const uint64_t c2x2 = f2_pack(c2, c2);
+    int steps = 0, outs = 0;
+    bool ok = true;
+    CrossItem w;
+    for (int i = blockIdx.x; ok && i < n_items; i += gridDim.x) {
+      w.at(W, i);
+      if (x >= w.tiles) continue;
+      const int T = key_steps(w), qrow = (w.tile + x) * 128 + row;
+      const bool in = qrow < W.Lq;
+      if (T > 0) {
+        const int buf = 2 * x + (outs & 1);
+        if (!__all_sync(0xffffffffu, mbar_wait(&d_full[buf], (outs >> 1) & 1, abort))) {
+          ok = false;
+          break;
+        }
+        const float2 rv = rowv[buf * 128 + row];
+        mbar_arrive(&d_empty[buf]);
+        const uint64_t nl2 = f2_pack(rv.x, rv.x);
+        float nd = rv.y;
+        for (int u = 0; u < T; ++u) {
+          if (!__all_sync(0xffffffffu, mbar_wait(&s_full[x], steps & 1, abort))) {
+            ok = false;
+            break;
+          }
+          ++steps;
+          fence_after_sync();
+          uint32_t s[64], dp[64];
+          tmem_ld32(sbase, s);
+          tmem_ld32(sbase + 32, s + 32);
+          tmem_ld32(sbase + 64, dp);
+          tmem_ld32(sbase + 96, dp + 32);
+          tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < 64; c += 2) {
+            const uint64_t t = ffma2(f2_pack(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), c2x2, nl2);
+            s[c] = __float_as_uint(ex2(f2_lo(t)));
+            s[c + 1] = __float_as_uint(ex2(f2_hi(t)));
+          }
+          const int valid = w.nv - u * 64;
+          if (valid < 64) {
+#pragma unroll
+            for (int c = 0; c < 64; ++c) s[c] = c < valid ? s[c] : 0u;
+          }
+          if (T == 1) {
+            float d0 = 0.f, d1 = 0.f;
+#pragma unroll
+            for (int c = 0; c < 64; c += 2) {
+              d0 = fmaf(__uint_as_float(s[c]), __uint_as_float(dp[c]), d0);
+              d1 = fmaf(__uint_as_float(s[c + 1]), __uint_as_float(dp[c + 1]), d1);
+            }
+            nd = -(d0 + d1);
+            if (in) a.delta[(int64_t)w.bh * W.Lq + qrow] = -nd;
+          }
+          const uint64_t nd2 = f2_pack(nd, nd);
+#pragma unroll
+          for (int c = 0; c < 64; c += 2) {
+            const uint64_t t = fadd2(f2_pack(__uint_as_float(dp[c]), __uint_as_float(dp[c + 1])), nd2);
+            const uint64_t z = fmul2(f2_pack(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), t);
+            s[c >> 1] = pack_bf16x2(f2_lo(z), f2_hi(z));
+          }
+          tmem_st32(sbase, s);
+          tmem_wait_st();
+          fence_before_sync();
+          mbar_arrive(&p_full[x]);
+        }
+        if (!ok) break;
+        if (!__all_sync(0xffffffffu, mbar_wait(&o_full[x], outs & 1, abort))) {
+          ok = false;
+          break;
+        }
+        ++outs;
+        fence_after_sync();
+      }
+      __nv_bfloat16* dst = a.dq + w.b * a.sdq.b + w.h * a.sdq.h + (int64_t)qrow * a.sdq.r;
+#pragma unroll 1
+      for (int ch = 0; ch < D / 32; ++ch) {
+        uint32_t o[32], pk[16];
+        if (T > 0) {
+          tmem_ld32(obase + ch * 32, o);
+          tmem_wait_ld();
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          pk[e] = T > 0 ? pack_bf16x2(__uint_as_float(o[2 * e]) * a.scale, __uint_as_float(o[2 * e + 1]) * a.scale) : 0u;
+        if (in) {
+          uint4* d4 = reinterpret_cast<uint4*>(dst + ch * 32);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) d4[e] = make_uint4(pk[4 * e], pk[4 * e + 1], pk[4 * e + 2], pk[4 * e + 3]);
+        }
+      }
+      fence_before_sync();
+    }
+  }
+
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  if (warp == 9) tmem_dealloc(tmem, 512);
+}
+
+// ------------------------------------------------------------------ dk, dv
+//
+// A CTA holds 128 keys and values and streams steps of 64 query rows:
+//   S^T = K Q^T, dP^T = V G^T (keys are TMEM lanes);  P^T and dS^T -> bf16 in
+//   place;  dV += P^T G,  dK += dS^T Q.
+// Even steps belong to warps 0-3, odd ones to warps 4-7, each with its own 128
+// columns of S^T and dP^T, so one's exponentials run under the other's MMAs.
+// TMEM columns: [128x, +64) S^T, [128x + 64, +64) dP^T, [256, +D) dV, [256 + D, +D) dK.
+//
+// Work: the (batch, key head, key tile) items times the steps of all query
+// rows of the heads that read them, laid end to end and cut into equal
+// contiguous ranges, one per CTA: every SM gets the same number of steps
+// whatever the numbers of heads and tiles, and no more than (items + CTAs)
+// pieces exist.  Piece (item i, CTA c) writes its 32-bit sums to slot i + c,
+// and cross_dkv_reduce_kernel adds an item's slots in order.
+struct CrossDkvArgs {
+  const float *lse, *delta;
+  const int32_t* count;  // allowed keys per batch entry, or null: Lk
+  float* part;           // [slots][2 (dv, dk)][128][D]
+  int batch, heads, kv_heads, Lq, Lk;
+  float scale_log2;
+};
+
+constexpr int kDkvStages = 4;
+
+template <int D>
+struct CrossDkvLayout {
+  static constexpr uint32_t kKeys = 128u * D * 2u;  // one of K, V
+  static constexpr uint32_t kHalf = 64u * D * 2u;   // one of Q, G of a step
+  static constexpr uint32_t kSlot = 2 * kHalf;
+  static constexpr int kNumBars = 2 * kDkvStages + 2 + 2 + 2 + 2 + 1 + 1;  // even: what follows is 16-byte aligned
+  static constexpr size_t bytes() {
+    return 1024 + 2 * kKeys + kDkvStages * kSlot + kNumBars * 8 + 16 + 8 * 2 * 128 * sizeof(float);
+  }
+};
+
+// The flat space of (item, step).
+struct CrossKeySpace {
+  int steps, per_head, group;
+  int64_t total;  // steps of all items
+  int64_t n;      // CTAs with work: each has at least one step
+  __device__ __forceinline__ static int tiles(const CrossDkvArgs& a, int b) {
+    return ((a.count == nullptr ? a.Lk : __ldg(a.count + b)) + 127) / 128;
+  }
+  __device__ __forceinline__ CrossKeySpace(const CrossDkvArgs& a, int ctas) {
+    group = a.heads / a.kv_heads;
+    per_head = (a.Lq + 63) / 64;
+    steps = per_head * group;
+    int64_t items = 0;
+    if (a.count == nullptr)
+      items = (int64_t)a.batch * tiles(a, 0);
+    else
+      for (int b = 0; b < a.batch; ++b) items += tiles(a, b);
+    total = items * a.kv_heads * steps;
+    n = min((int64_t)ctas, (total + 7) / 8);
+  }
+  __device__ __forceinline__ int64_t start(int64_t c) const { return c < n ? total * c / n : total; }
+  // the CTA whose range holds position x
+  __device__ __forceinline__ int64_t owner(int64_t x) const { return ((x + 1) * n - 1) / total; }
+};
+
+// A CTA's pieces in order: item `item` = key tile j of (b, hk), steps [u0, u0 + n).
+struct CrossPiece {
+  int64_t pos, end;
+  int item, b, hk, j, nv, u0, n;
+  int b_items;  // items of the batch entries before b
+  __device__ __forceinline__ CrossPiece(const CrossKeySpace& k) {
+    pos = k.start(blockIdx.x);
+    end = k.start(blockIdx.x + 1);
+    b = 0;
+    b_items = 0;
+  }
+  __device__ __forceinline__ bool next(const CrossKeySpace& k, const CrossDkvArgs& a) {
+    if (pos >= end) return false;
+    item = (int)(pos / k.steps);
+    u0 = (int)(pos % k.steps);
+    n = (int)min((int64_t)(k.steps - u0), end - pos);
+    pos += n;
+    int nt = CrossKeySpace::tiles(a, b);
+    while (item >= b_items + a.kv_heads * nt) {
+      b_items += a.kv_heads * nt;
+      nt = CrossKeySpace::tiles(a, ++b);
+    }
+    hk = (item - b_items) / nt;
+    j = (item - b_items) % nt;
+    nv = a.count == nullptr ? a.Lk : __ldg(a.count + b);
+    return true;
+  }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kCrossBwdThreads, 1)
+cross_dkv_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmG,
+                       const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                       const __grid_constant__ CrossDkvArgs a) {
+  using namespace sm100;
+  using Lay = CrossDkvLayout<D>;
+  constexpr int CB = D / 64, NS = kDkvStages;
+  constexpr uint32_t KEYS = Lay::kKeys, HALF = Lay::kHalf, SLOT = Lay::kSlot, DV = 256, DK = 256 + D;
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sKeys = smem;  // K, V
+  uint8_t* sRing = smem + 2 * KEYS;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sRing + NS * SLOT);
+  uint64_t* empty = full + NS;
+  uint64_t* kv_full = empty + NS;
+  uint64_t* kv_empty = kv_full + 1;
+  uint64_t* s_full = kv_empty + 1;  // [2]
+  uint64_t* p_full = s_full + 2;    // [2]
+  uint64_t* o_full = p_full + 2;
+  uint64_t* epi_done = o_full + 1;
+  uint64_t* mma_idle = epi_done + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(full + Lay::kNumBars);
+  volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  float* colv = reinterpret_cast<float*>(tmem_slot + 4);  // [8 warps][2 buffers][64 -lse2, 64 -delta]
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(kv_full, 1);
+    mbar_init(kv_empty, 1);
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&s_full[x], 1);
+      mbar_init(&p_full[x], 128);
+    }
+    mbar_init(o_full, 1);
+    mbar_init(epi_done, 256);
+    mbar_init(mma_idle, 1);
+    *abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  const CrossKeySpace ks(a, gridDim.x);
+  CrossPiece pc(ks);
+
+  if (warp == 8) {
+    // ================================================================ producer
+    if (lane == 0) {
+      prefetch_tensormap(&tmQ);
+      prefetch_tensormap(&tmG);
+      prefetch_tensormap(&tmK);
+      prefetch_tensormap(&tmV);
+      int it = 0, nkv = 0;
+      bool ok = true;
+      const bool packed = a.count != nullptr;
+      while (ok && pc.next(ks, a)) {
+        if (!(ok = mbar_wait(kv_empty, (nkv & 1) ^ 1, abort))) break;
+        mbar_expect_tx(kv_full, 2 * KEYS);
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb) {
+          const int c2 = packed ? pc.b * a.kv_heads + pc.hk : pc.hk, c3 = packed ? 0 : pc.b;
+          tma_load_4d(sKeys + cb * 128 * 128, &tmK, kv_full, cb * 64, pc.j * 128, c2, c3);
+          tma_load_4d(sKeys + KEYS + cb * 128 * 128, &tmV, kv_full, cb * 64, pc.j * 128, c2, c3);
+        }
+        ++nkv;
+        for (int t = 0; t < pc.n; ++t) {
+          const int s = it % NS, u = pc.u0 + t;
+          if (!(ok = mbar_wait(&empty[s], ((it / NS) & 1) ^ 1, abort))) break;
+          mbar_expect_tx(&full[s], SLOT);
+          const int h = pc.hk * ks.group + u / ks.per_head, row0 = u % ks.per_head * 64;
+#pragma unroll
+          for (int cb = 0; cb < CB; ++cb) {
+            uint8_t* dst = sRing + s * SLOT + cb * 64 * 128;
+            tma_load_4d(dst, &tmQ, &full[s], cb * 64, row0, h, pc.b);
+            tma_load_4d(dst + HALF, &tmG, &full[s], cb * 64, row0, h, pc.b);
+          }
+          ++it;
+        }
+      }
+      for (int u = it > NS ? it - NS : 0; u < it; ++u) mbar_drain(&full[u % NS], (u / NS) & 1);
+      if (nkv > 0) mbar_drain(kv_full, (nkv - 1) & 1);
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    // ================================================================ MMA issuer
+    constexpr uint32_t idS = idesc_bf16(128, 64, false, false);
+    constexpr uint32_t idO = idesc_bf16(128, D, false, true);
+    const uint32_t ring = smem_u32(sRing), keys = smem_u32(sKeys);
+    int it = 0, gs = 0, pieces = 0, waits[2] = {0, 0};
+    bool ok = true;
+    // S^T and dP^T of the next step into the columns of warpgroup x
+    auto s_mmas = [&](int x) {
+      const int s = it % NS;
+      if (!(ok = ok && mbar_wait(&full[s], (it / NS) & 1, abort))) return;
+      fence_after_sync();
+      ++it;
+      const uint32_t qb = ring + s * SLOT;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t ro = (kk >> 2) * 128 * 128 + (kk & 3) * 32, so = (kk >> 2) * 64 * 128 + (kk & 3) * 32;
+        mma_ss_warp(tmem + x * 128, desc_sw128(keys + ro, 16, 1024), desc_sw128(qb + so, 16, 1024), idS,
+                    kk > 0 ? 1u : 0u);
+      }
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t ro = (kk >> 2) * 128 * 128 + (kk & 3) * 32, so = (kk >> 2) * 64 * 128 + (kk & 3) * 32;
+        mma_ss_warp(tmem + x * 128 + 64, desc_sw128(keys + KEYS + ro, 16, 1024), desc_sw128(qb + HALF + so, 16, 1024),
+                    idS, kk > 0 ? 1u : 0u);
+      }
+      mma_commit_warp(&s_full[x]);
+    };
+    while (ok && pc.next(ks, a)) {
+      if (!(ok = mbar_wait(kv_full, pieces & 1, abort))) break;
+      fence_after_sync();
+      const int base = it;  // ring item of the piece's first step
+      for (int t = 0; ok && t < 2 && t < pc.n; ++t) s_mmas((gs + t) & 1);
+      for (int t = 0; ok && t < pc.n; ++t) {
+        const int x = (gs + t) & 1, s = (base + t) % NS;
+        if (!(ok = mbar_wait(&p_full[x], waits[x] & 1, abort))) break;
+        ++waits[x];
+        // the sums of the piece before have been read
+        if (t == 0 && pieces > 0 && !(ok = mbar_wait(epi_done, (pieces - 1) & 1, abort))) break;
+        fence_after_sync();
+        const uint32_t qb = ring + s * SLOT;
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          mma_ts_warp(tmem + DV, tmem + x * 128 + kk * 8, desc_sw128(qb + HALF + kk * 16 * 128, 64 * 128, 1024), idO,
+                      (t > 0 || kk > 0) ? 1u : 0u);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          mma_ts_warp(tmem + DK, tmem + x * 128 + 64 + kk * 8, desc_sw128(qb + kk * 16 * 128, 64 * 128, 1024), idO,
+                      (t > 0 || kk > 0) ? 1u : 0u);
+        mma_commit_warp(&empty[s]);
+        if (t + 2 < pc.n) s_mmas(x);
+      }
+      if (!ok) break;
+      mma_commit_warp(o_full);
+      mma_commit_warp(kv_empty);
+      gs += pc.n;
+      ++pieces;
+    }
+    mma_commit_warp(mma_idle);
+    mbar_drain(mma_idle, 0);
+    __syncwarp();
+  } else if (warp < 8) {
+    // ================================================================ keys as rows: even steps (warps 0-3), odd (4-7)
+    const int x = warp / 4, row = threadIdx.x % 128;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp % 4) * 32) << 16);
+    const uint32_t sbase = lane_base + x * 128;
+    const uint64_t c2x2 = f2_pack(a.scale_log2, a.scale_log2);
+    // Each warp keeps its own copy of a step's 64 -lse2 and -delta (two rows a
+    // lane, read one step ahead), so that no barrier but the bounded ones
+    // stands between warps.  A row past the end gives p = 0.
+    float* cv = colv + warp * 256;
+    auto columns = [&](int u) -> float4 {
+      const int q = u % ks.per_head * 64 + 2 * lane;
+      const int64_t at = ((int64_t)pc.b * a.heads + pc.hk * ks.group + u / ks.per_head) * a.Lq + q;
+      float4 v = make_float4(-INFINITY, -INFINITY, 0.f, 0.f);
+      if (q < a.Lq) {
+        v.x = -a.lse[at] * kLog2e;
+        v.z = -a.delta[at];
+      }
+      if (q + 1 < a.Lq) {
+        v.y = -a.lse[at + 1] * kLog2e;
+        v.w = -a.delta[at + 1];
+      }
+      return v;
+    };
+    int gs = 0, mine = 0, pieces = 0;
+    bool ok = true;
+    while (ok && pc.next(ks, a)) {
+      int t = (gs + x) & 1;  // this warpgroup's first step: gs + t has parity x
+      float4 cval = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (t < pc.n) cval = columns(pc.u0 + t);
+      for (; t < pc.n; t += 2, ++mine) {
+        float* cb = cv + (mine & 1) * 128;
+        *reinterpret_cast<float2*>(cb + 2 * lane) = make_float2(cval.x, cval.y);
+        *reinterpret_cast<float2*>(cb + 64 + 2 * lane) = make_float2(cval.z, cval.w);
+        __syncwarp();
+        if (t + 2 < pc.n) cval = columns(pc.u0 + t + 2);
+        if (!__all_sync(0xffffffffu, mbar_wait(&s_full[x], mine & 1, abort))) {
+          ok = false;
+          break;
+        }
+        fence_after_sync();
+        uint32_t s[64], dp[64];
+        tmem_ld32(sbase, s);
+        tmem_ld32(sbase + 32, s + 32);
+        tmem_ld32(sbase + 64, dp);
+        tmem_ld32(sbase + 96, dp + 32);
+        tmem_wait_ld();
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          uint32_t pk[16], dk[16];
+#pragma unroll
+          for (int c = 0; c < 32; c += 4) {
+            const ulonglong2 nl = *reinterpret_cast<const ulonglong2*>(cb + hh * 32 + c);
+            const ulonglong2 nd = *reinterpret_cast<const ulonglong2*>(cb + 64 + hh * 32 + c);
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
+              const int i = hh * 32 + c + e;
+              const uint64_t y = ffma2(f2_pack(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), c2x2,
+                                       e == 0 ? nl.x : nl.y);
+              const float p0 = ex2(f2_lo(y)), p1 = ex2(f2_hi(y));
+              const uint64_t g = fadd2(f2_pack(__uint_as_float(dp[i]), __uint_as_float(dp[i + 1])),
+                                       e == 0 ? nd.x : nd.y);
+              const uint64_t z = fmul2(f2_pack(p0, p1), g);
+              pk[(c + e) >> 1] = pack_bf16x2(p0, p1);
+              dk[(c + e) >> 1] = pack_bf16x2(f2_lo(z), f2_hi(z));
+            }
+          }
+          tmem_st16(sbase + hh * 16, pk);
+          tmem_st16(sbase + 64 + hh * 16, dk);
+        }
+        tmem_wait_st();
+        fence_before_sync();
+        mbar_arrive(&p_full[x]);
+      }
+      if (!ok) break;
+      gs += pc.n;
+      if (!__all_sync(0xffffffffu, mbar_wait(o_full, pieces & 1, abort))) break;
+      ++pieces;
+      fence_after_sync();
+      // warps 0-3 write dv, 4-7 dk
+      float* dst = a.part + (((int64_t)pc.item + blockIdx.x) * 2 + x) * 128 * D + row * D;
+      const bool in = pc.j * 128 + row < pc.nv;
+#pragma unroll 1
+      for (int ch = 0; ch < D / 32; ++ch) {
+        uint32_t o[32];
+        tmem_ld32(lane_base + (x == 0 ? DV : DK) + ch * 32, o);
+        tmem_wait_ld();
+        if (in) {
+          uint4* d4 = reinterpret_cast<uint4*>(dst + ch * 32);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) d4[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+        }
+      }
+      fence_before_sync();
+      mbar_arrive(epi_done);
+    }
+  }
+
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  if (warp == 9) tmem_dealloc(tmem, 512);
+}
+
+// dv (blockIdx.y = 0) and dk (1): the pieces of each key row in CTA order, the
+// scale, the rounding, and zeros where the key was not allowed.  `place`: packed
+// row of each key (null: the key's own).
+struct CrossReduceArgs {
+  CrossDkvArgs a;
+  const int32_t* place;
+  __nv_bfloat16 *dk, *dv;
+  HeadView sdk, sdv;
+  float scale;
+  int ctas;
+};
+
+template <int D>
+__global__ void __launch_bounds__(256) cross_dkv_reduce_kernel(const CrossReduceArgs r) {
+  const CrossDkvArgs& a = r.a;
+  const int64_t flat = (int64_t)blockIdx.x * (256 / (D / 4)) + threadIdx.x / (D / 4);
+  if (flat >= (int64_t)a.batch * a.kv_heads * a.Lk) return;
+  const int c = threadIdx.x % (D / 4) * 4;
+  const int j = (int)(flat % a.Lk), bh = (int)(flat / a.Lk), b = bh / a.kv_heads, hk = bh % a.kv_heads;
+  const int at = r.place == nullptr ? j : r.place[(int64_t)b * a.Lk + j];
+  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (at >= 0) {
+    const CrossKeySpace ks(a, r.ctas);
+    int64_t item = 0;
+    if (a.count == nullptr)
+      item = (int64_t)b * CrossKeySpace::tiles(a, 0);
+    else
+      for (int i = 0; i < b; ++i) item += CrossKeySpace::tiles(a, i);
+    item = item * a.kv_heads + hk * CrossKeySpace::tiles(a, b) + at / 128;
+    const int64_t first = ks.owner(item * ks.steps), last = ks.owner((item + 1) * ks.steps - 1);
+    for (int64_t s = first; s <= last; ++s) {
+      const float4 y = *reinterpret_cast<const float4*>(
+          a.part + (((item + s) * 2 + blockIdx.y) * 128 + at % 128) * D + c);
+      x.x += y.x;
+      x.y += y.y;
+      x.z += y.z;
+      x.w += y.w;
+    }
+  }
+  const float f = blockIdx.y == 0 ? 1.f : r.scale;
+  const HeadView& st = blockIdx.y == 0 ? r.sdv : r.sdk;
+  put4((blockIdx.y == 0 ? r.dv : r.dk) + b * st.b + hk * st.h + (int64_t)j * st.r + c, x.x * f, x.y * f, x.z * f,
+       x.w * f);
+}
+
+}  // namespace pisa

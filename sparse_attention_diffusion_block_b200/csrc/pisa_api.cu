@@ -12,6 +12,7 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include "common.cuh"
+#include "cross_bwd_sm100.cuh"
 #include "cross_simt.cuh"
 #include "cross_sm100.cuh"
 #include "fused_simt.cuh"
@@ -410,15 +411,15 @@ bool make_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, u
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// 4-D bf16 map over a strided [batch][heads][rows][inner] tensor, boxes of 128
-// rows by 64 swizzled elements; reads outside [0, rows) return zeros.
+// 4-D bf16 map over a strided [batch][heads][rows][inner] tensor, boxes of
+// `box_rows` rows by 64 swizzled elements; reads outside [0, rows) return zeros.
 bool make_map_view(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint64_t heads, uint64_t batch,
-                   const HeadView& v) {
+                   const HeadView& v, uint32_t box_rows) {
   EncodeTiled fn = encode_fn();
   if (!fn) return false;
   const cuuint64_t dims[4] = {inner, rows, heads, batch};
   const cuuint64_t strides[3] = {(cuuint64_t)v.r * 2, (cuuint64_t)v.h * 2, (cuuint64_t)v.b * 2};
-  const cuuint32_t box[4] = {64, 128, 1, 1};
+  const cuuint32_t box[4] = {64, box_rows, 1, 1};
   const cuuint32_t es[4] = {1, 1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, es,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,

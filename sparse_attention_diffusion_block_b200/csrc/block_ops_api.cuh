@@ -303,6 +303,14 @@ pisa_status run_cross_pack(const CrossArgs& a, const CrossShape& s, const CrossP
   return last_launch();
 }
 
+// The kernels that move registers between warpgroups wait for them: a launch
+// with fewer registers per thread than the split adds up to would never end.
+template <typename F>
+bool launch_registers(F* kernel, int least) {
+  cudaFuncAttributes at;
+  return cudaFuncGetAttributes(&at, kernel) == cudaSuccess && at.numRegs >= least;
+}
+
 bool sm_count(int* sms) {
   int dev = 0;
   return cudaGetDevice(&dev) == cudaSuccess &&
@@ -328,10 +336,11 @@ CrossFwdArgs cross_work(const CrossShape& s, const int32_t* count, int splits) {
 template <int D>
 pisa_status run_cross_fwd_sm100(const CrossArgs& a, const CrossShape& s, char* ws, cudaStream_t st) {
   const CrossFwdPlan p = cross_fwd_plan(s);
-  CUtensorMap mQ, mK, mV;
+  CUtensorMap mQ, mK, mV, mO;
   CrossKeys x;
   if (pisa_status e = run_cross_pack<D>(a, s, p.pack, ws, &x, st)) return e;
-  if (!make_map_view(&mQ, a.q, D, s.Lq, s.heads, s.batch, a.sq, 128) || !cross_key_maps<D>(x, 128, &mK, &mV))
+  if (!make_map_view(&mQ, a.q, D, s.Lq, s.heads, s.batch, a.sq, 128) ||
+      !make_map_view(&mO, a.out, D, s.Lq, s.heads, s.batch, a.so, 32) || !cross_key_maps<D>(x, 128, &mK, &mV))
     return PISA_ERR_CUDA;
   CrossFwdArgs f = cross_work(s, x.count, p.splits);
   f.out = static_cast<__nv_bfloat16*>(a.out);
@@ -342,8 +351,9 @@ pisa_status run_cross_fwd_sm100(const CrossArgs& a, const CrossShape& s, char* w
   int sms = 0;
   if (!sm_count(&sms)) return PISA_ERR_CUDA;
   const size_t smem = CrossFwdLayout<D>::bytes();
-  if (!set_smem(cross_fwd_sm100_kernel<D>, smem)) return PISA_ERR_CUDA;
-  cross_fwd_sm100_kernel<D><<<f.n_items < sms ? f.n_items : sms, kCrossFwdThreads, smem, st>>>(mQ, mK, mV, f);
+  static const bool regs = launch_registers(cross_fwd_sm100_kernel<D>, kCrossFwdRegs);
+  if (!regs || !set_smem(cross_fwd_sm100_kernel<D>, smem)) return PISA_ERR_CUDA;
+  cross_fwd_sm100_kernel<D><<<f.n_items < sms ? f.n_items : sms, kCrossFwdThreads, smem, st>>>(mQ, mK, mV, mO, f);
   if (last_launch() != PISA_OK || p.splits == 1) return last_launch();
   constexpr int rows = 256 / (D / 4);
   const long long n = ((long long)f.BH * s.Lq + rows - 1) / rows;
@@ -380,20 +390,26 @@ pisa_status run_cross_bwd_sm100(const CrossArgs& a, const CrossShape& s, char* w
     return PISA_ERR_CUDA;
   CrossDqArgs f{};
   f.dq = static_cast<__nv_bfloat16*>(a.dq);
-  f.g = static_cast<const __nv_bfloat16*>(a.g);
-  f.o = static_cast<const __nv_bfloat16*>(a.o);
   f.sdq = a.sdq;
-  f.sg = a.sg;
-  f.so = a.so;
   f.lse = a.lse;
   f.delta = reinterpret_cast<float*>(ws + p.pack.total);
   f.w = cross_work(s, x.count, 1);
   f.scale = a.scale;
+  if (s.Lk > 64) {  // up to 64 keys the dq kernel forms delta itself
+    const CrossDeltaArgs d{static_cast<const __nv_bfloat16*>(a.g), static_cast<const __nv_bfloat16*>(a.o), a.sg, a.so,
+                           f.delta, s.heads, s.Lq};
+    constexpr int rows = kDeltaRows * 256 / (D / 8);
+    cross_delta_kernel<D><<<dim3((s.Lq + rows - 1) / rows, s.batch * s.heads), 256, 0, st>>>(d);
+    if (last_launch() != PISA_OK) return PISA_ERR_CUDA;
+  }
   int sms = 0;
   if (!sm_count(&sms)) return PISA_ERR_CUDA;
   const size_t s1 = CrossDqLayout<D>::bytes(), s2 = CrossDkvLayout<D>::bytes();
-  if (!set_smem(cross_dq_sm100_kernel<D>, s1) || !set_smem(cross_dkv_sm100_kernel<D>, s2)) return PISA_ERR_CUDA;
-  cross_dq_sm100_kernel<D><<<f.w.n_items < sms ? f.w.n_items : sms, kCrossBwdThreads, s1, st>>>(q128, g128, k64, v64, f);
+  static const bool regs = launch_registers(cross_dq_sm100_kernel<D>, kCrossRegs512) &&
+                           launch_registers(cross_dkv_sm100_kernel<D>, kDkvRegs);
+  if (!regs || !set_smem(cross_dq_sm100_kernel<D>, s1) || !set_smem(cross_dkv_sm100_kernel<D>, s2))
+    return PISA_ERR_CUDA;
+  cross_dq_sm100_kernel<D><<<f.w.n_items < sms ? f.w.n_items : sms, kCrossThreads512, s1, st>>>(q128, g128, k64, v64, f);
   if (last_launch() != PISA_OK) return PISA_ERR_CUDA;
   CrossReduceArgs r{};
   r.a = CrossDkvArgs{a.lse, f.delta, x.count, reinterpret_cast<float*>(ws + p.pack.total + p.delta),
@@ -405,7 +421,7 @@ pisa_status run_cross_bwd_sm100(const CrossArgs& a, const CrossShape& s, char* w
   r.sdv = a.sdv;
   r.scale = a.scale;
   r.ctas = p.splits;
-  cross_dkv_sm100_kernel<D><<<p.splits, kCrossBwdThreads, s2, st>>>(q64, g64, k128, v128, r.a);
+  cross_dkv_sm100_kernel<D><<<p.splits, kDkvThreads, s2, st>>>(q64, g64, k128, v128, r.a);
   if (last_launch() != PISA_OK) return PISA_ERR_CUDA;
   constexpr int rows = 256 / (D / 4);
   const long long n = ((long long)s.batch * s.kv_heads * s.Lk + rows - 1) / rows;

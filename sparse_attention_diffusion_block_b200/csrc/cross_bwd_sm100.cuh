@@ -1,5 +1,5 @@
 // Gradients of the cross-attention on the 5th-generation tensor cores (bf16
-// inputs): one kernel for dq (and delta), one for dk and dv.
+// inputs): delta, then dq, then dk and dv.
 //
 // The scores and dp are formed twice, once with the queries and once with the
 // keys as accumulator rows: 7 products of Lq x Lk x d instead of 5.  In return
@@ -18,6 +18,55 @@ __device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
   return d;
 }
 
+// ------------------------------------------------------------------ delta
+//
+// delta_i = g_i . o_i: D / 8 lanes per row, four rows of a lane in flight.
+// Reads both once, bound by HBM.  (Inside the dq kernel two spare warps could
+// not read ahead fast enough, 64 KB a tile: 1.75 ms instead of 0.65 + 0.1 for
+// 32760 rows of 40 heads.)  Grid: (rows of one head, batch * heads).
+constexpr int kDeltaRows = 4;
+
+struct CrossDeltaArgs {
+  const __nv_bfloat16 *g, *o;
+  HeadView sg, so;
+  float* delta;
+  int heads, Lq;
+};
+
+template <int D>
+__global__ void __launch_bounds__(256) cross_delta_kernel(const CrossDeltaArgs a) {
+  constexpr int LPR = D / 8, RPB = 256 / LPR, U = kDeltaRows;
+  const int b = blockIdx.y / a.heads, h = blockIdx.y % a.heads;
+  const int first = blockIdx.x * (RPB * U) + threadIdx.x / LPR, c = threadIdx.x % LPR * 8;
+  const __nv_bfloat16* g = a.g + b * a.sg.b + h * a.sg.h + c;
+  const __nv_bfloat16* o = a.o + b * a.so.b + h * a.so.h + c;
+  uint4 y[U], z[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t r = first + u * RPB;
+    y[u] = z[u] = make_uint4(0, 0, 0, 0);
+    if (r < a.Lq) {
+      y[u] = *reinterpret_cast<const uint4*>(g + r * a.sg.r);
+      z[u] = *reinterpret_cast<const uint4*>(o + r * a.so.r);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const __nv_bfloat162* yy = reinterpret_cast<const __nv_bfloat162*>(&y[u]);
+    const __nv_bfloat162* zz = reinterpret_cast<const __nv_bfloat162*>(&z[u]);
+    float t = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 p = __bfloat1622float2(yy[e]), q = __bfloat1622float2(zz[e]);
+      t = fmaf(p.x, q.x, fmaf(p.y, q.y, t));
+    }
+#pragma unroll
+    for (int s = LPR / 2; s > 0; s >>= 1) t += __shfl_xor_sync(0xffffffffu, t, s);
+    const int r = first + u * RPB;
+    if (c == 0 && r < a.Lq) a.delta[(int64_t)blockIdx.y * a.Lq + r] = t;
+  }
+}
+
 // ------------------------------------------------------------------ dq
 //
 // Items: pairs of 128-row query tiles (A, B) of one head, key steps of 64.
@@ -29,79 +78,80 @@ __device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
 // one's exponentials run.  TMEM columns: [128x, +64) S_x, [128x + 64, +64) dP_x,
 // [256 + x D, +D) dQ_x.
 //
-// Warps 0-3 / 4-7: rows of tile A / B, 8: TMA producer, 9: MMA issuer, 10 / 11:
-// delta of tile A / B, one item ahead (delta_i = g_i . o_i, coalesced reads of
-// both, into shared memory and to global memory for the dk/dv kernel).  With a
-// single step of keys delta is instead sum_j p_ij dp_ij, formed in 32 bits from
-// what the row holds: with few keys ds is a small difference of dp and delta,
-// and the rounding of the stored bf16 output would dominate it (two keys:
-// error 1.7x that of the final rounding; 64 keys: 1 part in 24 of the variance).
+// Warps 0-3 / 4-7: rows of tile A / B, 8: TMA producer, 9: MMA issuer, 12-15:
+// epilogue (as in the forward kernel).  A key step's K stays until both tiles'
+// dQ have used it and its V only until both dP have, so K has three slots and V
+// two.  The queries and gradients of an item fill 128 KB and cannot be loaded
+// ahead; they are brought into L2 one item early.
+//
+// delta_i = g_i . o_i comes from cross_delta_kernel, except with a single step
+// of keys: there it is sum_j p_ij dp_ij, formed in 32 bits from what the row
+// holds (and written for the dk/dv kernel).  With few keys ds is a small
+// difference of dp and delta, and the rounding of the stored bf16 output would
+// dominate it (two keys: 1.7 times the error of the final rounding); with 64
+// keys it adds one part in 24 to the variance.
 struct CrossDqArgs {
   __nv_bfloat16* dq;
-  const __nv_bfloat16 *g, *o;
-  HeadView sdq, sg, so;
+  HeadView sdq;
   const float* lse;
   float* delta;
   CrossFwdArgs w;  // shape of the work: heads, kv_heads, Lq, Lk, pairs, count (splits = 1)
   float scale;
 };
 
-constexpr int kCrossBwdThreads = 384, kDqStages = 5;
+constexpr int kDqK = 3, kDqV = 2;
 
 template <int D>
 struct CrossDqLayout {
   static constexpr uint32_t kRows = 128u * D * 2u;  // one of Q, G of a tile
   static constexpr uint32_t kSlot = 64u * D * 2u;   // one of K, V of a step
-  static constexpr int kNumBars = 2 * kDqStages + 2 + 2 + 2 + 2 + 2 + 4 + 4 + 1;
+  static constexpr uint32_t kStage = 4 * 4096;      // output rows of the four epilogue warps
+  static constexpr int kNumBars = 2 * (kDqK + kDqV) + 13;
   static constexpr size_t bytes() {
-    return 1024 + 4 * kRows + kDqStages * kSlot + kNumBars * 8 + 16 + 4 * 128 * 8;
+    return 1024 + 4 * kRows + (kDqK + kDqV) * kSlot + kStage + kNumBars * 8 + 16;
   }
 };
 
 template <int D>
-__global__ void __launch_bounds__(kCrossBwdThreads, 1)
+__global__ void __launch_bounds__(kCrossThreads512, 1)
 cross_dq_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmG,
                       const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                       const __grid_constant__ CrossDqArgs a) {
   using namespace sm100;
   using Lay = CrossDqLayout<D>;
-  constexpr int CB = D / 64, NS = kDqStages;
+  constexpr int CB = D / 64, NK = kDqK, NV = kDqV;
   constexpr uint32_t ROWS = Lay::kRows, SLOT = Lay::kSlot, OC = 256;
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sRows = smem;  // Q_A, G_A, Q_B, G_B
-  uint8_t* sRing = smem + 4 * ROWS;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sRing + NS * SLOT);
-  uint64_t* empty = full + NS;
-  uint64_t* q_full = empty + NS;     // [2]
+  uint8_t* sK = smem + 4 * ROWS;
+  uint8_t* sV = sK + NK * SLOT;
+  uint8_t* sStage = sV + NV * SLOT;
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(sStage + Lay::kStage);
+  uint64_t* k_empty = k_full + NK;
+  uint64_t* v_full = k_empty + NK;
+  uint64_t* v_empty = v_full + NV;
+  uint64_t* q_full = v_empty + NV;   // [2]
   uint64_t* q_empty = q_full + 2;    // [2]
   uint64_t* s_full = q_empty + 2;    // [2]
   uint64_t* p_full = s_full + 2;     // [2]
   uint64_t* o_full = p_full + 2;     // [2]
-  uint64_t* d_full = o_full + 2;     // [2 tiles][2 buffers]
-  uint64_t* d_empty = d_full + 4;    // [2][2]
-  uint64_t* mma_idle = d_empty + 4;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(full + Lay::kNumBars);
+  uint64_t* o_empty = o_full + 2;    // [2]
+  uint64_t* mma_idle = o_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(k_full + Lay::kNumBars);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  float2* rowv = reinterpret_cast<float2*>(tmem_slot + 4);  // [2 tiles][2 buffers][128]: (-lse2, -delta)
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < NS; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
-    }
+    for (int s = 0; s < 2 * NK + 2 * NV; ++s) mbar_init(&k_full[s], 1);  // k_full .. v_empty
     for (int x = 0; x < 2; ++x) {
       mbar_init(&q_full[x], 1);
       mbar_init(&q_empty[x], 1);
       mbar_init(&s_full[x], 1);
       mbar_init(&p_full[x], 128);
       mbar_init(&o_full[x], 1);
-      for (int y = 0; y < 2; ++y) {
-        mbar_init(&d_full[2 * x + y], 32);
-        mbar_init(&d_empty[2 * x + y], 128);
-      }
+      mbar_init(&o_empty[x], 128);
     }
     mbar_init(mma_idle, 1);
     *abort = 0;
@@ -120,7 +170,9 @@ cross_dq_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
   // An item's key steps of 64 (CrossItem counts tiles of 128).
   auto key_steps = [](const CrossItem& w) { return (w.nv + 63) / 64; };
 
-  if (warp == 8) {
+  if (warp >= 8 && warp < 12) {
+   fewer_registers<96>();
+   if (warp == 8) {
     // ================================================================ producer
     if (lane == 0) {
       prefetch_tensormap(&tmQ);
@@ -130,58 +182,77 @@ cross_dq_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
       int it = 0, nq[2] = {0, 0};
       bool ok = true;
       const bool packed = W.count != nullptr;
-      auto load = [&](const CUtensorMap* map, const CrossItem& w, int u) {
-        const int s = it % NS;
-        if (!(ok = ok && mbar_wait(&empty[s], ((it / NS) & 1) ^ 1, abort))) return;
-        mbar_expect_tx(&full[s], SLOT);
+      auto load = [&](const CrossItem& w, int u) {
+        const int sk = it % NK, sv = it % NV;
+        const int c2 = packed ? w.b * W.kv_heads + w.hk : w.hk, c3 = packed ? 0 : w.b;
+        if (!(ok = ok && mbar_wait(&k_empty[sk], ((it / NK) & 1) ^ 1, abort))) return;
+        mbar_expect_tx(&k_full[sk], SLOT);
 #pragma unroll
         for (int cb = 0; cb < CB; ++cb)
-          tma_load_4d(sRing + s * SLOT + cb * 64 * 128, map, &full[s], cb * 64, u * 64,
-                      packed ? w.b * W.kv_heads + w.hk : w.hk, packed ? 0 : w.b);
+          tma_load_4d(sK + sk * SLOT + cb * 64 * 128, &tmK, &k_full[sk], cb * 64, u * 64, c2, c3);
+        if (!(ok = mbar_wait(&v_empty[sv], ((it / NV) & 1) ^ 1, abort))) {
+          mbar_drain(&k_full[sk], (it / NK) & 1);  // the one copy that the counts below do not cover
+          return;
+        }
+        mbar_expect_tx(&v_full[sv], SLOT);
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb)
+          tma_load_4d(sV + sv * SLOT + cb * 64 * 128, &tmV, &v_full[sv], cb * 64, u * 64, c2, c3);
         ++it;
       };
-      auto load_rows = [&](const CrossItem& w) {
-        for (int x = 0; ok && x < w.tiles; ++x) {
-          if (!(ok = mbar_wait(&q_empty[x], (nq[x] & 1) ^ 1, abort))) return;
-          mbar_expect_tx(&q_full[x], 2 * ROWS);
+      auto load_rows = [&](const CrossItem& w, int x) {
+        if (x >= w.tiles || !(ok = ok && mbar_wait(&q_empty[x], (nq[x] & 1) ^ 1, abort))) return;
+        mbar_expect_tx(&q_full[x], 2 * ROWS);
 #pragma unroll
-          for (int cb = 0; cb < CB; ++cb) {
-            uint8_t* dst = sRows + 2 * x * ROWS + cb * 128 * 128;
-            tma_load_4d(dst, &tmQ, &q_full[x], cb * 64, (w.tile + x) * 128, w.h, w.b);
-            tma_load_4d(dst + ROWS, &tmG, &q_full[x], cb * 64, (w.tile + x) * 128, w.h, w.b);
-          }
-          ++nq[x];
+        for (int cb = 0; cb < CB; ++cb) {
+          uint8_t* dst = sRows + 2 * x * ROWS + cb * 128 * 128;
+          tma_load_4d(dst, &tmQ, &q_full[x], cb * 64, (w.tile + x) * 128, w.h, w.b);
+          tma_load_4d(dst + ROWS, &tmG, &q_full[x], cb * 64, (w.tile + x) * 128, w.h, w.b);
         }
+        ++nq[x];
       };
-      CrossItem cur;
+      CrossItem cur, nxt;
       int i = blockIdx.x;
-      while (ok && cur.with_keys(W, i)) {
+      bool has = cur.with_keys(W, i);
+      while (ok && has) {
         // the first keys of an item are loaded while the last item's queries
-        // are in use, its queries as their buffers become free
-        load(&tmK, cur, 0);
-        load(&tmV, cur, 0);
-        load_rows(cur);
-        for (int u = 1; ok && u < key_steps(cur); ++u) {
-          load(&tmK, cur, u);
-          load(&tmV, cur, u);
-        }
+        // are in use, its queries as their buffers become free, and the second
+        // keys before the 64 KB of tile B, which are needed later
+        load(cur, 0);
+        load_rows(cur, 0);
+        if (key_steps(cur) > 1) load(cur, 1);
+        load_rows(cur, 1);
         i += gridDim.x;
+        has = nxt.with_keys(W, i);
+        if (has) {
+          for (int x = 0; x < nxt.tiles; ++x)
+#pragma unroll
+            for (int cb = 0; cb < CB; ++cb) {
+              tma_prefetch_4d(&tmQ, cb * 64, (nxt.tile + x) * 128, nxt.h, nxt.b);
+              tma_prefetch_4d(&tmG, cb * 64, (nxt.tile + x) * 128, nxt.h, nxt.b);
+            }
+        }
+        for (int u = 2; ok && u < key_steps(cur); ++u) load(cur, u);
+        cur = nxt;
       }
-      for (int u = it > NS ? it - NS : 0; u < it; ++u) mbar_drain(&full[u % NS], (u / NS) & 1);
+      for (int u = it > NK ? it - NK : 0; u < it; ++u) mbar_drain(&k_full[u % NK], (u / NK) & 1);
+      for (int u = it > NV ? it - NV : 0; u < it; ++u) mbar_drain(&v_full[u % NV], (u / NV) & 1);
       for (int x = 0; x < 2; ++x)
         if (nq[x] > 0) mbar_drain(&q_full[x], (nq[x] - 1) & 1);
     }
     __syncwarp();
-  } else if (warp == 9) {
+   } else if (warp == 9) {
     // ================================================================ MMA issuer
     constexpr uint32_t idS = idesc_bf16(128, 64, false, false);
     constexpr uint32_t idO = idesc_bf16(128, D, false, true);
-    const uint32_t ring = smem_u32(sRing), rows = smem_u32(sRows);
-    int it = 0, steps[2] = {0, 0}, nq[2] = {0, 0};
+    const uint32_t kring = smem_u32(sK), vring = smem_u32(sV), rows = smem_u32(sRows);
+    int it = 0, steps[2] = {0, 0}, nq[2] = {0, 0}, outs[2] = {0, 0};
     bool ok = true;
-    auto take = [&](int& s) {
-      s = it % NS;
-      if (!(ok = ok && mbar_wait(&full[s], (it / NS) & 1, abort))) return;
+    auto take = [&](int& k, int& v) {
+      k = it % NK;
+      v = it % NV;
+      if (!(ok = ok && mbar_wait(&k_full[k], (it / NK) & 1, abort))) return;
+      if (!(ok = mbar_wait(&v_full[v], (it / NV) & 1, abort))) return;
       fence_after_sync();
       ++it;
     };
@@ -192,7 +263,7 @@ cross_dq_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
         ++nq[x];
         fence_after_sync();
       }
-      const uint32_t qb = rows + 2 * x * ROWS, kb = ring + ks * SLOT, vb = ring + vs * SLOT;
+      const uint32_t qb = rows + 2 * x * ROWS, kb = kring + ks * SLOT, vb = vring + vs * SLOT;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         const uint32_t ro = (kk >> 2) * 128 * 128 + (kk & 3) * 32, so = (kk >> 2) * 64 * 128 + (kk & 3) * 32;
@@ -211,10 +282,9 @@ cross_dq_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
     int i = blockIdx.x, ks = 0, vs = 0;
     bool has = cur.with_keys(W, i);
     if (has) {
-      take(ks);
-      take(vs);
+      take(ks, vs);
       for (int x = 0; ok && x < cur.tiles; ++x) s_mmas(x, ks, vs, true, key_steps(cur) == 1);
-      if (ok) mma_commit_warp(&empty[vs]);
+      if (ok) mma_commit_warp(&v_empty[vs]);
     }
     while (ok && has) {
       i += gridDim.x;
@@ -223,16 +293,15 @@ cross_dq_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
       for (int u = 0; ok && u < T; ++u) {
         const bool last = u + 1 == T, next = !last || more;
         const int k0 = ks;
-        if (next) {
-          take(ks);
-          take(vs);
-        }
+        if (next) take(ks, vs);
         for (int x = 0; ok && x < 2; ++x) {
           if (x < cur.tiles) {
             if (!(ok = mbar_wait(&p_full[x], steps[x] & 1, abort))) break;
             ++steps[x];
+            // the item before has been read out of dQ
+            if (u == 0 && outs[x]++ > 0 && !(ok = mbar_wait(&o_empty[x], outs[x] & 1, abort))) break;
             fence_after_sync();
-            const uint32_t kb = ring + k0 * SLOT;
+            const uint32_t kb = kring + k0 * SLOT;
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
               mma_ts_warp(tmem + OC + x * D, tmem + x * 128 + kk * 8, desc_sw128(kb + kk * 16 * 128, 64 * 128, 1024), idO,
@@ -246,8 +315,8 @@ cross_dq_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
           }
         }
         if (!ok) break;
-        mma_commit_warp(&empty[k0]);
-        if (next) mma_commit_warp(&empty[vs]);
+        mma_commit_warp(&k_empty[k0]);
+        if (next) mma_commit_warp(&v_empty[vs]);
       }
       cur = nxt;
       has = more;
@@ -255,155 +324,110 @@ cross_dq_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
     mma_commit_warp(mma_idle);
     mbar_drain(mma_idle, 0);
     __syncwarp();
-  } else if (warp >= 10) {
-    // ================================================================ delta, one item ahead
-    const int x = warp - 10;
-    constexpr int LPR = D / 8, RPL = 32 / LPR;  // lanes per row, rows per load
-    int n = 0;
-    bool ok = true;
-    CrossItem w;
-    for (int i = blockIdx.x; ok && i < n_items; i += gridDim.x) {
-      w.at(W, i);
-      if (x >= w.tiles || w.T == 0) continue;
-      const int buf = n & 1;
-      if (!__all_sync(0xffffffffu, mbar_wait(&d_empty[2 * x + buf], ((n >> 1) & 1) ^ 1, abort))) {
-        ok = false;
-        break;
-      }
-      ++n;
-      float2* dst = rowv + (2 * x + buf) * 128;
-      const int row0 = (w.tile + x) * 128;
-      const int64_t flat = (int64_t)w.bh * W.Lq + row0;
-      const bool from_o = key_steps(w) > 1;
-      const __nv_bfloat16* g = a.g + w.b * a.sg.b + w.h * a.sg.h + (int64_t)row0 * a.sg.r + lane % LPR * 8;
-      const __nv_bfloat16* o = a.o + w.b * a.so.b + w.h * a.so.h + (int64_t)row0 * a.so.r + lane % LPR * 8;
-      for (int r0 = 0; r0 < 128; r0 += 32) {
-        float mine = 0.f;  // delta of row r0 + lane
-        if (from_o) {
-#pragma unroll 4
-          for (int k = 0; k < 32 / RPL; ++k) {
-            const int r = r0 + k * RPL + lane / LPR;
-            float t = 0.f;
-            if (row0 + r < W.Lq) {
-              float y[8], z[8];
-              load8(g + (int64_t)r * a.sg.r, y);
-              load8(o + (int64_t)r * a.so.r, z);
-#pragma unroll
-              for (int e = 0; e < 8; ++e) t = fmaf(y[e], z[e], t);
-            }
-#pragma unroll
-            for (int s = LPR / 2; s > 0; s >>= 1) t += __shfl_xor_sync(0xffffffffu, t, s);
-            const float got = __shfl_sync(0xffffffffu, t, (lane % RPL) * LPR);
-            if (lane / RPL == k) mine = got;
-          }
-        }
-        const int r = r0 + lane;
-        float nl = -INFINITY;
-        if (row0 + r < W.Lq) {
-          nl = -a.lse[flat + r] * kLog2e;
-          if (from_o) a.delta[flat + r] = mine;
-        }
-        dst[r] = make_float2(nl, -mine);
-      }
-      mbar_arrive(&d_full[2 * x + buf]);
-    }
-  } else {
+   }
+  } else if (warp < 8) {
+    more_registers<152>();
     // ================================================================ rows of tile A (warps 0-3), B (4-7)
     const int x = warp / 4, row = threadIdx.x % 128;
-    const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp % 4) * 32) << 16);
-    const uint32_t sbase = lane_base + x * 128, obase = lane_base + OC + x * D;
+    const uint32_t sbase = tmem + (static_cast<uint32_t>((warp % 4) * 32) << 16) + x * 128;
     const float c2 = W.scale_log2;
     const uint64_t c2x2 = f2_pack(c2, c2);
-    int steps = 0, outs = 0;
+    int steps = 0;
     bool ok = true;
-    CrossItem w;
-    for (int i = blockIdx.x; ok && i < n_items; i += gridDim.x) {
-      w.at(W, i);
-      if (x >= w.tiles) continue;
-      const int T = key_steps(w), qrow = (w.tile + x) * 128 + row;
-      const bool in = qrow < W.Lq;
-      if (T > 0) {
-        const int buf = 2 * x + (outs & 1);
-        if (!__all_sync(0xffffffffu, mbar_wait(&d_full[buf], (outs >> 1) & 1, abort))) {
+    CrossItem w, nxt;
+    // -lse2 and -delta of this thread's row, read one item ahead; a row past
+    // the end gives p = 0
+    float nl = -INFINITY, nd = 0.f;
+    auto row_values = [&](const CrossItem& v) {
+      const int qrow = (v.tile + x) * 128 + row;
+      const bool in = x < v.tiles && qrow < W.Lq;
+      const int64_t flat = (int64_t)v.bh * W.Lq + qrow;
+      nl = in ? -a.lse[flat] * kLog2e : -INFINITY;
+      nd = in && key_steps(v) > 1 ? -a.delta[flat] : 0.f;
+    };
+    int i = blockIdx.x;
+    bool has = w.with_keys(W, i);
+    if (has) row_values(w);
+    while (ok && has) {
+      i += gridDim.x;
+      has = nxt.with_keys(W, i);
+      const uint64_t nl2 = f2_pack(nl, nl);
+      float mine = nd;
+      if (has) row_values(nxt);
+      const int T = x < w.tiles ? key_steps(w) : 0;
+      for (int u = 0; u < T; ++u) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&s_full[x], steps & 1, abort))) {
           ok = false;
           break;
         }
-        const float2 rv = rowv[buf * 128 + row];
-        mbar_arrive(&d_empty[buf]);
-        const uint64_t nl2 = f2_pack(rv.x, rv.x);
-        float nd = rv.y;
-        for (int u = 0; u < T; ++u) {
-          if (!__all_sync(0xffffffffu, mbar_wait(&s_full[x], steps & 1, abort))) {
+        ++steps;
+        fence_after_sync();
+        uint32_t s[64], dp[64];
+        tmem_ld32(sbase, s);
+        tmem_ld32(sbase + 32, s + 32);
+        tmem_ld32(sbase + 64, dp);
+        tmem_ld32(sbase + 96, dp + 32);
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 64; c += 2) {
+          const uint64_t t = ffma2(f2_pack(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), c2x2, nl2);
+          s[c] = __float_as_uint(ex2(f2_lo(t)));
+          s[c + 1] = __float_as_uint(ex2(f2_hi(t)));
+        }
+        const int valid = w.nv - u * 64;
+        if (valid < 64) {
+#pragma unroll
+          for (int c = 0; c < 64; ++c) s[c] = c < valid ? s[c] : 0u;
+        }
+        if (T == 1) {
+          float d0 = 0.f, d1 = 0.f;
+#pragma unroll
+          for (int c = 0; c < 64; c += 2) {
+            d0 = fmaf(__uint_as_float(s[c]), __uint_as_float(dp[c]), d0);
+            d1 = fmaf(__uint_as_float(s[c + 1]), __uint_as_float(dp[c + 1]), d1);
+          }
+          mine = -(d0 + d1);
+          const int qrow = (w.tile + x) * 128 + row;
+          if (qrow < W.Lq) a.delta[(int64_t)w.bh * W.Lq + qrow] = -mine;
+        }
+        const uint64_t nd2 = f2_pack(mine, mine);
+#pragma unroll
+        for (int c = 0; c < 64; c += 2) {
+          const uint64_t t = fadd2(f2_pack(__uint_as_float(dp[c]), __uint_as_float(dp[c + 1])), nd2);
+          const uint64_t z = fmul2(f2_pack(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), t);
+          s[c >> 1] = pack_bf16x2(f2_lo(z), f2_hi(z));
+        }
+        tmem_st32(sbase, s);
+        tmem_wait_st();
+        fence_before_sync();
+        mbar_arrive(&p_full[x]);
+      }
+      w = nxt;
+    }
+  } else {
+    fewer_registers<112>();
+    // ================================================================ epilogue: dq = s dQ (0 without keys)
+    const int quarter = warp - 12;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    int outs[2] = {0, 0};
+    bool ok = true;
+    CrossItem w;
+    for (int i = blockIdx.x; ok && i < n_items; i += gridDim.x) {
+      w.at(W, i);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        if (x >= w.tiles) continue;
+        const int row0 = (w.tile + x) * 128 + quarter * 32;
+        if (w.T > 0) {
+          if (!__all_sync(0xffffffffu, mbar_wait(&o_full[x], outs[x]++ & 1, abort))) {
             ok = false;
             break;
           }
-          ++steps;
           fence_after_sync();
-          uint32_t s[64], dp[64];
-          tmem_ld32(sbase, s);
-          tmem_ld32(sbase + 32, s + 32);
-          tmem_ld32(sbase + 64, dp);
-          tmem_ld32(sbase + 96, dp + 32);
-          tmem_wait_ld();
-#pragma unroll
-          for (int c = 0; c < 64; c += 2) {
-            const uint64_t t = ffma2(f2_pack(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), c2x2, nl2);
-            s[c] = __float_as_uint(ex2(f2_lo(t)));
-            s[c + 1] = __float_as_uint(ex2(f2_hi(t)));
-          }
-          const int valid = w.nv - u * 64;
-          if (valid < 64) {
-#pragma unroll
-            for (int c = 0; c < 64; ++c) s[c] = c < valid ? s[c] : 0u;
-          }
-          if (T == 1) {
-            float d0 = 0.f, d1 = 0.f;
-#pragma unroll
-            for (int c = 0; c < 64; c += 2) {
-              d0 = fmaf(__uint_as_float(s[c]), __uint_as_float(dp[c]), d0);
-              d1 = fmaf(__uint_as_float(s[c + 1]), __uint_as_float(dp[c + 1]), d1);
-            }
-            nd = -(d0 + d1);
-            if (in) a.delta[(int64_t)w.bh * W.Lq + qrow] = -nd;
-          }
-          const uint64_t nd2 = f2_pack(nd, nd);
-#pragma unroll
-          for (int c = 0; c < 64; c += 2) {
-            const uint64_t t = fadd2(f2_pack(__uint_as_float(dp[c]), __uint_as_float(dp[c + 1])), nd2);
-            const uint64_t z = fmul2(f2_pack(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), t);
-            s[c >> 1] = pack_bf16x2(f2_lo(z), f2_hi(z));
-          }
-          tmem_st32(sbase, s);
-          tmem_wait_st();
-          fence_before_sync();
-          mbar_arrive(&p_full[x]);
         }
-        if (!ok) break;
-        if (!__all_sync(0xffffffffu, mbar_wait(&o_full[x], outs & 1, abort))) {
-          ok = false;
-          break;
-        }
-        ++outs;
-        fence_after_sync();
+        store_tile<D>(lane_base + OC + x * D, w.T > 0, a.scale, &o_empty[x], sStage + quarter * 4096,
+                      a.dq + w.b * a.sdq.b + w.h * a.sdq.h + (int64_t)row0 * a.sdq.r, a.sdq.r, W.Lq - row0, lane);
       }
-      __nv_bfloat16* dst = a.dq + w.b * a.sdq.b + w.h * a.sdq.h + (int64_t)qrow * a.sdq.r;
-#pragma unroll 1
-      for (int ch = 0; ch < D / 32; ++ch) {
-        uint32_t o[32], pk[16];
-        if (T > 0) {
-          tmem_ld32(obase + ch * 32, o);
-          tmem_wait_ld();
-        }
-#pragma unroll
-        for (int e = 0; e < 16; ++e)
-          pk[e] = T > 0 ? pack_bf16x2(__uint_as_float(o[2 * e]) * a.scale, __uint_as_float(o[2 * e + 1]) * a.scale) : 0u;
-        if (in) {
-          uint4* d4 = reinterpret_cast<uint4*>(dst + ch * 32);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) d4[e] = make_uint4(pk[4 * e], pk[4 * e + 1], pk[4 * e + 2], pk[4 * e + 3]);
-        }
-      }
-      fence_before_sync();
     }
   }
 
@@ -436,7 +460,7 @@ struct CrossDkvArgs {
   float scale_log2;
 };
 
-constexpr int kDkvStages = 4;
+constexpr int kDkvStages = 4, kDkvThreads = 384, kDkvRegs = 168;
 
 template <int D>
 struct CrossDkvLayout {
@@ -504,7 +528,7 @@ struct CrossPiece {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kCrossBwdThreads, 1)
+__global__ void __launch_bounds__(kDkvThreads, 1)
 cross_dkv_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmG,
                        const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                        const __grid_constant__ CrossDkvArgs a) {
@@ -559,7 +583,10 @@ cross_dkv_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
   const CrossKeySpace ks(a, gridDim.x);
   CrossPiece pc(ks);
 
-  if (warp == 8) {
+  // Registers: 2 x 128 x 208 + 128 x 88 = 384 x 168, the launch total.
+  if (warp >= 8) {
+   asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n" ::: "memory");
+   if (warp == 8) {
     // ================================================================ producer
     if (lane == 0) {
       prefetch_tensormap(&tmQ);
@@ -597,7 +624,7 @@ cross_dkv_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       if (nkv > 0) mbar_drain(kv_full, (nkv - 1) & 1);
     }
     __syncwarp();
-  } else if (warp == 9) {
+   } else if (warp == 9) {
     // ================================================================ MMA issuer
     constexpr uint32_t idS = idesc_bf16(128, 64, false, false);
     constexpr uint32_t idO = idesc_bf16(128, D, false, true);
@@ -658,7 +685,9 @@ cross_dkv_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
     mma_commit_warp(mma_idle);
     mbar_drain(mma_idle, 0);
     __syncwarp();
-  } else if (warp < 8) {
+   }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;\n" ::: "memory");
     // ================================================================ keys as rows: even steps (warps 0-3), odd (4-7)
     const int x = warp / 4, row = threadIdx.x % 128;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp % 4) * 32) << 16);

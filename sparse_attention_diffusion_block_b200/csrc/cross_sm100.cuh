@@ -91,21 +91,24 @@ __global__ void __launch_bounds__(kPackThreads) cross_pack_kernel(const CrossPac
 // Persistent CTAs, one per SM, walk items: a pair of consecutive 128-row query
 // tiles (A, B) of one head, and, where there are fewer pairs than SMs, one of
 // `splits` shares of that head's key tiles.  Warp roles as in the fused
-// self-attention kernel: warps 0-3 softmax of tile A, 4-7 of tile B (a thread
-// per query row = TMEM lane), warp 8 TMA producer, warp 9 MMA issuer, 10-11
-// idle.  S = Q K^T, then P (bf16, over S in TMEM) and O += P V; both tiles use
-// each key and value tile, loaded once into a ring of four 128-row slots.
+// self-attention kernel: warps 0-3 / 4-7 softmax of tile A / B, a thread per
+// query row (= TMEM lane), warp 8 TMA producer, warp 9 MMA issuer, 10-11 idle.
+// S = Q K^T, then P (bf16, over S in TMEM) and O += P V; both tiles use each
+// key and value tile, loaded once into a ring of three 128-row slots.
 //
 // Text has few keys (4 tiles of 128 for 512), so an item is short and what
 // counts is that items follow each other without a gap: the issuer runs one
-// item's last P V and the next item's first Q K^T back to back, the Q tiles
-// rotate through three buffers (A of the next item is loaded while both tiles
-// of this one are in use; B's takes the buffer that A's last S has left), and
-// a tile's epilogue overlaps the other tile's MMAs.
+// item's last P V and the next item's first Q K^T back to back, the next Q
+// tiles are in L2 by then, and outputs leave by TMA from shared memory of their
+// own while the softmax goes on.  75600 x 512, 40 heads of 128: 1.19 ms with
+// 16-byte stores of each thread's row, 0.85 ms with whole lines through shared
+// memory, which still held the softmax warps up for 3400 of 18100 cycles an
+// item.  (Four more warps for the epilogue took registers from the softmax and
+// the issuer: 1.13 ms.)
 //
 // TMEM columns: [0,128) S_A, [128,256) S_B, [256,256+D) O_A, [256+D,256+2D) O_B.
 struct CrossFwdArgs {
-  __nv_bfloat16* out;
+  __nv_bfloat16* out;    // splits > 1: for the join
   HeadView so;
   float* lse;            // [batch * heads][Lq] or null
   const int32_t* count;  // allowed keys per batch entry, or null: Lk
@@ -115,14 +118,69 @@ struct CrossFwdArgs {
   float scale_log2;
 };
 
-constexpr int kCrossStages = 4, kCrossQBufs = 3, kCrossFwdThreads = 384;
+constexpr int kCrossStages = 3, kCrossFwdThreads = 384, kCrossFwdRegs = 168;
+constexpr int kCrossThreads512 = 512, kCrossRegs512 = 128;
+
+// Registers of the four warpgroups: two of rows, producer / issuer, epilogue.
+// R + R + I + E may add up to the 4 x 128 that the block is launched with.
+template <int R>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(R) : "memory");
+}
+template <int R>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(R) : "memory");
+}
+
+// A warp's 32 rows of an accumulator tile (D 32-bit columns of TMEM from
+// obase, a lane per row), scaled row by row and rounded to bf16, to global
+// memory; zeros without work.  Arrives on `read` once TMEM has been read.  64
+// columns at a time go through 4 KB of the warp's shared memory (16-byte units
+// swizzled by row, no bank conflicts either way), so that a store instruction
+// writes four whole 128-byte lines instead of sixteen bytes of 32 rows.
+template <int D>
+__device__ __forceinline__ void store_tile(uint32_t obase, bool work, float f, uint64_t* read, uint8_t* stage,
+                                           __nv_bfloat16* dst, int64_t pitch, int rows, int lane) {
+#pragma unroll 1
+  for (int ch = 0; ch < D / 64; ++ch) {
+#pragma unroll
+    for (int hh = 0; hh < 2; ++hh) {
+      uint32_t o[32];
+      sm100::tmem_ld32(obase + ch * 64 + hh * 32, o);  // without work whatever is there: replaced
+      sm100::tmem_wait_ld();
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t pk[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float x = __uint_as_float(o[8 * c + 2 * e]) * f, y = __uint_as_float(o[8 * c + 2 * e + 1]) * f;
+          pk[e] = work ? sm100::pack_bf16x2(x, y) : 0u;
+        }
+        *reinterpret_cast<uint4*>(stage + lane * 128 + (((hh * 4 + c) ^ (lane & 7)) << 4)) =
+            make_uint4(pk[0], pk[1], pk[2], pk[3]);
+      }
+    }
+    if (work && ch == D / 64 - 1) {
+      sm100::fence_before_sync();
+      sm100::mbar_arrive(read);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = 4 * i + lane / 8, c = lane % 8;
+      const uint4 x = *reinterpret_cast<const uint4*>(stage + r * 128 + ((c ^ (r & 7)) << 4));
+      if (r < rows) *reinterpret_cast<uint4*>(dst + r * pitch + ch * 64 + c * 8) = x;
+    }
+    __syncwarp();
+  }
+}
 
 template <int D>
 struct CrossFwdLayout {
   static constexpr uint32_t kTile = 128u * D * 2u;
-  static constexpr int kNumBars = 2 * kCrossStages + 2 * kCrossQBufs + 7;
-  static constexpr size_t bytes() {
-    return 1024 + (kCrossStages + kCrossQBufs) * kTile + kNumBars * 8 + 16;
+  static constexpr int kNumBars = 2 * kCrossStages + 11;
+  static constexpr size_t bytes() {  // Q and output of both tiles, the ring
+    return 1024 + (4 + kCrossStages) * kTile + kNumBars * 8 + 16;
   }
 };
 
@@ -134,9 +192,9 @@ struct CrossItem {
     const int p = i / a.splits;
     bh = p / a.pairs;
     tile = 2 * (p % a.pairs);
-    tiles = min(2, (a.Lq + 127) / 128 - tile);
     b = bh / a.heads;
     h = bh % a.heads;
+    tiles = min(2, (a.Lq + 127) / 128 - tile);
     hk = h / (a.heads / a.kv_heads);
     nv = a.count == nullptr ? a.Lk : __ldg(a.count + b);
     const int nt = (nv + 127) / 128;
@@ -156,21 +214,23 @@ struct CrossItem {
 template <int D>
 __global__ void __launch_bounds__(kCrossFwdThreads, 1)
 cross_fwd_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                       const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CrossFwdArgs a) {
+                       const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
+                       const __grid_constant__ CrossFwdArgs a) {
   using namespace sm100;
   using Lay = CrossFwdLayout<D>;
-  constexpr int CB = D / 64, NS = kCrossStages, NQ = kCrossQBufs;
+  constexpr int CB = D / 64, NS = kCrossStages;
   constexpr uint32_t TILE = Lay::kTile, OC = 256;
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;
-  uint8_t* sRing = smem + NQ * TILE;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sRing + NS * TILE);
+  uint8_t* sRing = smem + 2 * TILE;
+  uint8_t* sOut = sRing + NS * TILE;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sOut + 2 * TILE);
   uint64_t* empty = full + NS;
-  uint64_t* q_full = empty + NS;
-  uint64_t* q_empty = q_full + NQ;
-  uint64_t* s_full = q_empty + NQ;  // [2]
+  uint64_t* q_full = empty + NS;    // [2]
+  uint64_t* q_empty = q_full + 2;   // [2]
+  uint64_t* s_full = q_empty + 2;   // [2]
   uint64_t* p_full = s_full + 2;    // [2]
   uint64_t* o_full = p_full + 2;    // [2]
   uint64_t* mma_idle = o_full + 2;
@@ -183,11 +243,9 @@ cross_fwd_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
-    for (int s = 0; s < NQ; ++s) {
-      mbar_init(&q_full[s], 1);
-      mbar_init(&q_empty[s], 1);
-    }
     for (int x = 0; x < 2; ++x) {
+      mbar_init(&q_full[x], 1);
+      mbar_init(&q_empty[x], 1);
       mbar_init(&s_full[x], 1);
       mbar_init(&p_full[x], 128);
       mbar_init(&o_full[x], 1);
@@ -207,14 +265,14 @@ cross_fwd_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
 
   // Registers: 2 x 128 x 200 + 128 x 104 = 384 x 168, the launch total.
   if (warp >= 8) {
-   asm volatile("setmaxnreg.dec.sync.aligned.u32 104;\n" ::: "memory");
+   fewer_registers<104>();
    if (warp == 8) {
     // ================================================================ producer
     if (lane == 0) {
       prefetch_tensormap(&tmQ);
       prefetch_tensormap(&tmK);
       prefetch_tensormap(&tmV);
-      int it = 0, nq = 0;  // ring items and Q tiles loaded
+      int it = 0, nq[2] = {0, 0};  // ring items and Q tiles loaded
       bool ok = true;
       const bool packed = a.count != nullptr;
       auto load = [&](const CUtensorMap* map, const CrossItem& w, int j) {
@@ -229,13 +287,12 @@ cross_fwd_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
         ++it;
       };
       auto load_q = [&](const CrossItem& w, int x) {
-        const int s = nq % NQ;
-        if (!(ok = ok && mbar_wait(&q_empty[s], ((nq / NQ) & 1) ^ 1, abort))) return;
-        mbar_expect_tx(&q_full[s], TILE);
+        if (x >= w.tiles || !(ok = ok && mbar_wait(&q_empty[x], (nq[x] & 1) ^ 1, abort))) return;
+        mbar_expect_tx(&q_full[x], TILE);
 #pragma unroll
         for (int cb = 0; cb < CB; ++cb)
-          tma_load_4d(sQ + s * TILE + cb * 128 * 128, &tmQ, &q_full[s], cb * 64, (w.tile + x) * 128, w.h, w.b);
-        ++nq;
+          tma_load_4d(sQ + x * TILE + cb * 128 * 128, &tmQ, &q_full[x], cb * 64, (w.tile + x) * 128, w.h, w.b);
+        ++nq[x];
       };
       CrossItem cur, nxt;
       int i = blockIdx.x;
@@ -243,20 +300,25 @@ cross_fwd_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       if (has) {
         load_q(cur, 0);
         load(&tmK, cur, 0);
-        if (cur.tiles > 1) load_q(cur, 1);
+        load_q(cur, 1);
       }
       while (ok && has) {
         i += gridDim.x;
         const bool more = nxt.with_keys(a, i);
+        if (more)
+          for (int x = 0; x < nxt.tiles; ++x)
+#pragma unroll
+            for (int cb = 0; cb < CB; ++cb) tma_prefetch_4d(&tmQ, cb * 64, (nxt.tile + x) * 128, nxt.h, nxt.b);
         for (int u = 0; ok && u < cur.T; ++u) {
-          const bool last = u + 1 == cur.T;
-          if (last && more) load_q(nxt, 0);
           load(&tmV, cur, u);
-          if (!last) {
+          if (u + 1 < cur.T) {
             load(&tmK, cur, u + 1);
           } else if (more) {
+            // the tiles' buffers are free after their last S, one step before
+            // the next item's first
             load(&tmK, nxt, 0);
-            if (nxt.tiles > 1) load_q(nxt, 1);
+            load_q(nxt, 0);
+            load_q(nxt, 1);
           }
         }
         cur = nxt;
@@ -264,7 +326,8 @@ cross_fwd_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       }
       // the copies already issued land before the CTA can exit
       for (int u = it > NS ? it - NS : 0; u < it; ++u) mbar_drain(&full[u % NS], (u / NS) & 1);
-      for (int u = nq > NQ ? nq - NQ : 0; u < nq; ++u) mbar_drain(&q_full[u % NQ], (u / NQ) & 1);
+      for (int x = 0; x < 2; ++x)
+        if (nq[x] > 0) mbar_drain(&q_full[x], (nq[x] - 1) & 1);
     }
     __syncwarp();
    } else if (warp == 9) {
@@ -274,7 +337,7 @@ cross_fwd_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
     constexpr uint32_t idS = idesc_bf16(128, 128, false, false);
     constexpr uint32_t idO = idesc_bf16(128, D, false, true);
     const uint32_t ring = smem_u32(sRing), qbase = smem_u32(sQ);
-    int it = 0, steps[2] = {0, 0};
+    int it = 0, steps[2] = {0, 0}, nq[2] = {0, 0};
     bool ok = true;
     auto take = [&](int& s) {
       s = it % NS;
@@ -282,13 +345,14 @@ cross_fwd_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       fence_after_sync();
       ++it;
     };
-    auto wait_q = [&](int n) {
-      if (!(ok = ok && mbar_wait(&q_full[n % NQ], (n / NQ) & 1, abort))) return;
-      fence_after_sync();
-    };
-    // S_x = Q K^T with Q tile number n; `done`: the tile's last one
-    auto s_mmas = [&](int x, int n, int ks, bool done) {
-      const uint32_t qb = qbase + (n % NQ) * TILE, kb = ring + ks * TILE;
+    // S_x = Q K^T; first / last: of the tile's item
+    auto s_mmas = [&](int x, int ks, bool first, bool last) {
+      if (first) {
+        if (!(ok = ok && mbar_wait(&q_full[x], nq[x] & 1, abort))) return;
+        ++nq[x];
+        fence_after_sync();
+      }
+      const uint32_t qb = qbase + x * TILE, kb = ring + ks * TILE;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         const uint32_t off = (kk >> 2) * 128 * 128 + (kk & 3) * 32;
@@ -296,23 +360,19 @@ cross_fwd_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
                     kk > 0 ? 1u : 0u);
       }
       mma_commit_warp(&s_full[x]);
-      if (done) mma_commit_warp(&q_empty[n % NQ]);
+      if (last) mma_commit_warp(&q_empty[x]);
     };
     CrossItem cur, nxt;
-    int i = blockIdx.x, nq = 0, ks = 0, vs = 0;
+    int i = blockIdx.x, ks = 0, vs = 0;
     bool has = cur.with_keys(a, i);
     if (has) {
       take(ks);
-      for (int x = 0; ok && x < cur.tiles; ++x) {
-        wait_q(x);
-        if (ok) s_mmas(x, x, ks, cur.T == 1);
-      }
+      for (int x = 0; ok && x < cur.tiles; ++x) s_mmas(x, ks, true, cur.T == 1);
       if (ok) mma_commit_warp(&empty[ks]);
     }
     while (ok && has) {
       i += gridDim.x;
       const bool more = nxt.with_keys(a, i);
-      const int nq2 = nq + cur.tiles;
       for (int u = 0; ok && u < cur.T; ++u) {
         const bool last = u + 1 == cur.T;
         const bool next = !last || more;  // S tiles follow
@@ -331,10 +391,9 @@ cross_fwd_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
             if (last) mma_commit_warp(&o_full[x]);
           }
           if (!last) {
-            if (x < cur.tiles) s_mmas(x, nq + x, ks, u + 2 == cur.T);
+            if (x < cur.tiles) s_mmas(x, ks, false, u + 2 == cur.T);
           } else if (more && x < nxt.tiles) {
-            wait_q(nq2 + x);
-            if (ok) s_mmas(x, nq2 + x, ks, nxt.T == 1);
+            s_mmas(x, ks, true, nxt.T == 1);
           }
         }
         if (!ok) break;
@@ -342,7 +401,6 @@ cross_fwd_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
         if (next) mma_commit_warp(&empty[ks]);
       }
       cur = nxt;
-      nq = nq2;
       has = more;
     }
     // every MMA issued completes before TMEM is freed
@@ -351,18 +409,24 @@ cross_fwd_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
     __syncwarp();
    }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;\n" ::: "memory");
+    more_registers<200>();
     // ================================================================ softmax: tile A (warps 0-3), B (4-7)
-    const int x = warp / 4, row = threadIdx.x % 128;
+    const int x = warp / 4;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp % 4) * 32) << 16);
     const uint32_t sbase = lane_base + x * 128, obase = lane_base + OC + x * D;
     const float c2 = a.scale_log2;
     int steps = 0, outs = 0;
     bool ok = true;
-    CrossItem w;
+    uint8_t* stage = sOut + x * TILE + warp % 4 * (TILE / 4);  // this warp's 32 output rows
+    CrossItem w, nxt;
+    nxt.at(a, blockIdx.x);
     for (int i = blockIdx.x; ok && i < a.n_items; i += gridDim.x) {
-      w.at(a, i);
-      if (x >= w.tiles) continue;
+      w = nxt;
+      const bool more = i + (int)gridDim.x < a.n_items;
+      if (x >= w.tiles) {
+        if (more) nxt.at(a, i + gridDim.x);
+        continue;
+      }
       float m = -INFINITY, l = 0.f;
       uint32_t s[128];
       for (int u = 0; u < w.T; ++u) {
@@ -435,7 +499,13 @@ cross_fwd_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
         mbar_arrive(&p_full[x]);
       }
       if (!ok) break;
+      if (more) nxt.at(a, i + gridDim.x);  // its divisions run while P V does
       // epilogue: o = O / l (0 without keys)
+      const int row0 = (w.tile + x) * 128 + warp % 4 * 32, qrow = row0 + lane;
+      const bool in = qrow < a.Lq;
+      const float inv = w.T > 0 ? 1.f / l : 0.f;
+      const float lse2 = w.T > 0 ? m + log2f(l) : -INFINITY;
+      const int64_t flat = (int64_t)w.bh * a.Lq + qrow;
       if (w.T > 0) {
         if (!__all_sync(0xffffffffu, mbar_wait(&o_full[x], outs & 1, abort))) {
           ok = false;
@@ -444,11 +514,6 @@ cross_fwd_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
         ++outs;
         fence_after_sync();
       }
-      const int qrow = (w.tile + x) * 128 + row;
-      const bool in = qrow < a.Lq;
-      const float inv = w.T > 0 ? 1.f / l : 0.f;
-      const float lse2 = w.T > 0 ? m + log2f(l) : -INFINITY;
-      const int64_t flat = (int64_t)w.bh * a.Lq + qrow;
       if (a.splits > 1) {
         const int64_t at = (int64_t)w.split * a.BH * a.Lq + flat;
         if (in) a.part_lse[at] = lse2;
@@ -468,26 +533,36 @@ cross_fwd_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
         }
       } else {
         if (in && a.lse != nullptr) a.lse[flat] = lse2 * 0.6931471805599453f;
-        __nv_bfloat16* dst = a.out + w.b * a.so.b + w.h * a.so.h + (int64_t)qrow * a.so.r;
+        if (lane == 0) tma_store_wait_read();  // the last item's rows have left
+        __syncwarp();
 #pragma unroll 1
         for (int ch = 0; ch < D / 32; ++ch) {
-          uint32_t o[32], pk[16];
-          if (w.T > 0) {
-            tmem_ld32(obase + ch * 32, o);
-            tmem_wait_ld();
-          }
+          uint32_t o[32];
+          tmem_ld32(obase + ch * 32, o);  // without keys whatever is there: replaced
+          tmem_wait_ld();
+          uint8_t* to = stage + (ch >> 1) * 4096 + lane * 128;
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            pk[e] = w.T > 0 ? pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv) : 0u;
-          if (in) {
-            uint4* d4 = reinterpret_cast<uint4*>(dst + ch * 32);
+          for (int c = 0; c < 4; ++c) {
+            uint32_t pk[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) d4[e] = make_uint4(pk[4 * e], pk[4 * e + 1], pk[4 * e + 2], pk[4 * e + 3]);
+            for (int e = 0; e < 4; ++e)
+              pk[e] = w.T > 0 ? pack_bf16x2(__uint_as_float(o[8 * c + 2 * e]) * inv,
+                                            __uint_as_float(o[8 * c + 2 * e + 1]) * inv)
+                              : 0u;
+            *reinterpret_cast<uint4*>(to + ((((ch & 1) * 4 + c) ^ (lane & 7)) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
           }
+        }
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0 && row0 < a.Lq) {
+#pragma unroll
+          for (int cb = 0; cb < CB; ++cb) tma_store_4d(&tmO, stage + cb * 4096, cb * 64, row0, w.h, w.b);
+          tma_store_commit();
         }
       }
       fence_before_sync();  // before this tile's next P releases the P V that overwrites O
     }
+    if (lane == 0) tma_store_wait();
   }
 
   fence_before_sync();

@@ -408,7 +408,7 @@ pisa_status pisa_rope(const void* q, void* q_out, const void* k, void* k_out, pi
 
 /* Scratch bytes of pisa_cross_attn_fwd (backward = 0) or pisa_cross_attn_bwd
  * (backward = 1); masked: whether kv_len or key_mask is given.  0 for an
- * unsupported shape; a forward may need none, which is returned as 16. */
+ * unsupported shape; 16 where none is needed, and then workspace may be NULL. */
 size_t pisa_cross_workspace_size(pisa_dtype dtype, int batch, int heads, int kv_heads, int Lq, int Lk, int d,
                                  int masked, int backward);
 

@@ -399,48 +399,69 @@ def tuning_load(path: str):
 
 
 class _LaunchOn:
-    """The stream and device that a call launches and allocates on: ``stream``,
-    or the current stream of the tensors' device.  Tensors made here for
-    another stream than the current one are kept from reuse until both are
-    done with them (keep())."""
+    """Where a call launches and allocates: ``stream``, or the current stream
+    of the tensors' device.  ``handle`` is the raw stream; within the context
+    the device and stream are current.  Tensors made for another stream than
+    the caller's are kept from reuse until both are done with them (keep())."""
+
+    __slots__ = ("handle", "ctx", "caller")
 
     def __init__(self, device: torch.device, stream: Optional[torch.cuda.Stream]):
-        self.current = torch.cuda.current_stream(device)
-        self.stream = self.current if stream is None else stream
-        if self.stream.device != device:
+        self.ctx = self.caller = None
+        if stream is None and torch.cuda.current_device() == device.index:
+            self.handle = torch._C._cuda_getCurrentRawStream(device.index)
+            return
+        caller = torch.cuda.current_stream(device)
+        if stream is None:
+            stream = caller
+        elif stream.device != device:
             raise ValueError("stream is not on the tensors' device")
-        self.other = self.stream != self.current
-        self.ctx = (torch.cuda.stream(self.stream)
-                    if self.other or torch.cuda.current_device() != device.index else None)
+        elif stream != caller:
+            self.caller = caller
+        self.handle = stream.cuda_stream
+        self.ctx = torch.cuda.stream(stream)
 
     def __enter__(self):
         if self.ctx is not None:
             self.ctx.__enter__()
-        return ctypes.c_void_p(self.stream.cuda_stream)
+        return self
 
     def __exit__(self, *exc):
         if self.ctx is not None:
             self.ctx.__exit__(*exc)
 
     def keep(self, *tensors):
-        if self.other:
+        if self.caller is not None:
             for t in tensors:
-                t.record_stream(self.current)
+                if t is not None:
+                    t.record_stream(self.caller)
 
 
-def _same_kind(first: torch.Tensor, *others: torch.Tensor) -> None:
+def _same_kind(first: torch.Tensor, *others: Optional[torch.Tensor]) -> None:
+    dtype, device = first.dtype, first.device
+    if device.type != "cuda":
+        raise ValueError("tensors must be CUDA tensors")
     for t in (first,) + others:
-        if not t.is_cuda or t.dim() != 4 or t.stride(3) != 1 and t.shape[3] != 1:
-            raise ValueError("tensors must be 4-d CUDA tensors with a contiguous last dimension")
-        if t.dtype != first.dtype or t.device != first.device:
+        if t is None:
+            continue
+        if t.dim() != 4 or t.stride(3) != 1 and t.shape[3] != 1:
+            raise ValueError("tensors must be 4-d with a contiguous last dimension")
+        if t.dtype != dtype or t.device != device:
             raise ValueError("tensors must share one dtype and one device")
 
 
+def _at(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+@functools.lru_cache(maxsize=1024)
+def _stride_array(*strides):
+    """pisa_strides of tensors with these strides (a function of the numbers alone)."""
+    return (_Strides * len(strides))(*[s[:3] for s in strides])
+
+
 def _strides(*ts: Optional[torch.Tensor]):
-    """pisa_strides of the tensors, or None when all are dense."""
-    if all(t is None or t.is_contiguous() for t in ts):
-        return None
-    return (_Strides * len(ts))(*[(0, 0, 0) if t is None else t.stride()[:3] for t in ts])
+    return _stride_array(*[(0, 0, 0) if t is None else t.stride() for t in ts])
 
 
 @functools.lru_cache(maxsize=256)
@@ -457,7 +478,7 @@ def _rope_plan(axis_dims: Tuple[int, ...], theta: float, layout: str, scaling: s
 
 def _rope(q, k, positions, axis_dims, theta, layout, scaling, factor, original_len, q_out, k_out, stream, backward):
     plan = _rope_plan(tuple(axis_dims), float(theta), layout, scaling, float(factor), int(original_len))
-    _same_kind(q, *(t for t in (k, q_out, k_out) if t is not None))
+    _same_kind(q, k, q_out, k_out)
     b, h, L, d = q.shape
     code = _dtype_code(q)
     if k is not None and (k.shape[0] != b or k.shape[2:] != q.shape[2:]):
@@ -465,22 +486,21 @@ def _rope(q, k, positions, axis_dims, theta, layout, scaling, factor, original_l
     for x, y in ((q, q_out), (k, k_out)):
         if y is not None and (x is None or y.shape != x.shape):
             raise ValueError("an output has the shape of its input")
+    axes = plan.axes
     if (positions.dtype != torch.float32 or positions.device != q.device or not positions.is_contiguous()
-            or positions.shape not in ((L, plan.axes), (b, L, plan.axes))):
+            or positions.shape not in ((L, axes), (b, L, axes))):
         raise ValueError("positions must be contiguous float32 [L, axes] or [batch, L, axes] on the same device")
-    on = _LaunchOn(q.device, stream)
-    with on as st:
-        made = []
-        if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-            made.append(q_out)
-        if k is not None and k_out is None:
-            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-            made.append(k_out)
-        _check(_lib_rope(_ptr(q), _ptr(q_out), _ptr(k), _ptr(k_out), code, b, h,
-                         0 if k is None else k.shape[1], L, d, _strides(q, q_out, k, k_out), _ptr(positions),
-                         L * plan.axes if positions.dim() == 3 else 0, ctypes.byref(plan), backward, st), "pisa_rope")
-    on.keep(*made)
+    new_q, new_k = q_out is None, k is not None and k_out is None
+    with _LaunchOn(q.device, stream) as on:
+        if new_q:
+            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        if new_k:
+            k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
+        _check(_lib_rope(q.data_ptr(), q_out.data_ptr(), _at(k), _at(k_out), code, b, h,
+                         0 if k is None else k.shape[1], L, d, _strides(q, q_out, k, k_out), positions.data_ptr(),
+                         L * axes if positions.dim() == 3 else 0, ctypes.byref(plan), backward, on.handle),
+               "pisa_rope")
+    on.keep(q_out if new_q else None, k_out if new_k else None)
     return q_out, k_out
 
 
@@ -511,6 +531,20 @@ def cross_workspace_size(dtype: torch.dtype, batch, heads, kv_heads, Lq, Lk, d, 
     return int(_lib_cross_ws(code, batch, heads, kv_heads, Lq, Lk, d, 1 if masked else 0, 1 if backward else 0))
 
 
+@functools.lru_cache(maxsize=1024)
+def _cross_need(*shape) -> int:
+    return int(_lib_cross_ws(*shape))
+
+
+def _cross_workspace(need: int, device, given: Optional[torch.Tensor]):
+    """(tensor or None, address, bytes) of the scratch; none is made for the calls that need none."""
+    if given is None:
+        if need <= 16:
+            return None, None, 0
+        given = torch.empty(need, dtype=torch.uint8, device=device)
+    return given, given.data_ptr(), given.numel() * given.element_size()
+
+
 def _cross_shapes(q, k, v, kv_len, key_mask):
     b, h, Lq, d = q.shape
     hk, Lk = k.shape[1], k.shape[2]
@@ -539,26 +573,23 @@ def cross_attn_fwd(q, k, v, kv_len=None, key_mask=None, return_lse=False, out=No
     keys gives 0.  With ``return_lse``: (out, lse), lse float32 [b,h,Lq], as
     cross_attn_bwd needs it.  Any strides with a contiguous last dimension that
     are multiples of 16 bytes."""
-    _same_kind(q, k, v, *(() if out is None else (out,)))
+    _same_kind(q, k, v, out)
     code = _dtype_code(q)
     b, h, hk, Lq, Lk, d = _cross_shapes(q, k, v, kv_len, key_mask)
     if out is not None and out.shape != q.shape:
         raise ValueError("out has the shape of q")
     masked = 0 if kv_len is None and key_mask is None else 1
-    on = _LaunchOn(q.device, stream)
-    with on as st:
-        made = []
-        if out is None:
+    lse, new = None, out is None
+    with _LaunchOn(q.device, stream) as on:
+        if new:
             out = _like(q)
-            made.append(out)
-        lse = torch.empty(b, h, Lq, dtype=torch.float32, device=q.device) if return_lse else None
         if return_lse:
-            made.append(lse)
-        ws = _workspace(_lib_cross_ws(code, b, h, hk, Lq, Lk, d, masked, 0), q.device, workspace)
-        _check(_lib_cross_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), code, b, h, hk, Lq, Lk, d,
-                              _strides(q, k, v, out), _ptr(kv_len), _ptr(key_mask), _ptr(ws), ws.numel(), st),
+            lse = torch.empty(b, h, Lq, dtype=torch.float32, device=q.device)
+        _ws, at, size = _cross_workspace(_cross_need(code, b, h, hk, Lq, Lk, d, masked, 0), q.device, workspace)
+        _check(_lib_cross_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _at(lse), code, b, h, hk, Lq,
+                              Lk, d, _strides(q, k, v, out), _at(kv_len), _at(key_mask), at, size, on.handle),
                "pisa_cross_attn_fwd")
-    on.keep(*made)
+    on.keep(out if new else None, lse)
     return (out, lse) if return_lse else out
 
 
@@ -567,7 +598,7 @@ def cross_attn_bwd(dout, q, k, v, out, lse, kv_len=None, key_mask=None, dq=None,
     """(dq, dk, dv) of cross_attn_fwd from the gradient of its output, with its
     out, lse and mask.  dk and dv are sums over the query heads that share a
     key head."""
-    _same_kind(dout, q, k, v, out, *(t for t in (dq, dk, dv) if t is not None))
+    _same_kind(q, dout, k, v, out, dq, dk, dv)
     code = _dtype_code(q)
     b, h, hk, Lq, Lk, d = _cross_shapes(q, k, v, kv_len, key_mask)
     for x, y in ((dout, q), (out, q), (dq, q), (dk, k), (dv, v)):
@@ -576,22 +607,19 @@ def cross_attn_bwd(dout, q, k, v, out, lse, kv_len=None, key_mask=None, dq=None,
     if lse.dtype != torch.float32 or lse.shape != (b, h, Lq) or not lse.is_contiguous() or lse.device != q.device:
         raise ValueError("lse must be contiguous float32 [b,h,Lq] on the same device")
     masked = 0 if kv_len is None and key_mask is None else 1
-    on = _LaunchOn(q.device, stream)
-    with on as st:
-        made = []
+    made = [None, None, None]
+    with _LaunchOn(q.device, stream) as on:
         if dq is None:
-            dq = _like(q)
-            made.append(dq)
+            made[0] = dq = _like(q)
         if dk is None:
-            dk = _like(k)
-            made.append(dk)
+            made[1] = dk = _like(k)
         if dv is None:
-            dv = _like(v)
-            made.append(dv)
-        ws = _workspace(_lib_cross_ws(code, b, h, hk, Lq, Lk, d, masked, 1), q.device, workspace)
-        _check(_lib_cross_bwd(_ptr(dout), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(dq), _ptr(dk),
-                              _ptr(dv), code, b, h, hk, Lq, Lk, d, _strides(dout, q, k, v, out, dq, dk, dv),
-                              _ptr(kv_len), _ptr(key_mask), _ptr(ws), ws.numel(), st), "pisa_cross_attn_bwd")
+            made[2] = dv = _like(v)
+        _ws, at, size = _cross_workspace(_cross_need(code, b, h, hk, Lq, Lk, d, masked, 1), q.device, workspace)
+        _check(_lib_cross_bwd(dout.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+                              lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), code, b, h, hk, Lq, Lk, d,
+                              _strides(dout, q, k, v, out, dq, dk, dv), _at(kv_len), _at(key_mask), at, size,
+                              on.handle), "pisa_cross_attn_bwd")
     on.keep(*made)
     return dq, dk, dv
 

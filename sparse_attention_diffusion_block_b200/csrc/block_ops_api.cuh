@@ -80,15 +80,16 @@ bool rope_plan_ok(const pisa_rope_plan* p) {
   return true;
 }
 
+// Tokens per block: as many as one step of its threads takes (whole pieces of
+// 4 KB on the [batch, heads, L, d] side), fewer where that gives less than 32
+// blocks per SM, four rounds of what is resident (9973 tokens, 96 heads: 96 us;
+// with eight blocks per SM 110, with four 133).
 template <typename T, bool HALF, int V>
-pisa_status launch_rope(const RopeArgs& a, int batch, cudaStream_t st) {
-  const int tokens = kRopeThreads / (a.d / (HALF ? 2 * V : V));
-  const int gx = (a.L + tokens - 1) / tokens, rows = a.q.heads + a.k.heads;
-  // Head groups: enough blocks for eight per SM (2048 threads), no more, since
-  // each group forms the angles again.
-  const long long want = (8LL * kSMs + (long long)gx * batch - 1) / ((long long)gx * batch);
-  const int gy = (int)(want < 1 ? 1 : want > rows ? rows : want);
-  rope_kernel<T, HALF, V><<<dim3(gx, gy, batch), kRopeThreads, 0, st>>>(a);
+pisa_status launch_rope(RopeArgs a, int batch, cudaStream_t st) {
+  a.tokens = kRopeThreads / (a.d / (HALF ? 2 * V : V));
+  while (a.tokens > 1 && (long long)((a.L + a.tokens - 1) / a.tokens) * batch < 32LL * kSMs) a.tokens /= 2;
+  const size_t smem = (size_t)a.tokens * a.pairs * sizeof(float2);
+  rope_kernel<T, HALF, V><<<dim3((a.L + a.tokens - 1) / a.tokens, batch), kRopeThreads, smem, st>>>(a);
   return last_launch();
 }
 
@@ -177,22 +178,48 @@ CrossPackPlan cross_pack_plan(const CrossShape& s, bool backward) {
   return p;
 }
 
+// Few query rows per key head go through cross_rows_kernel.
+// Few query rows per key head go through cross_rows_kernel: with bf16 one (80
+// heads of 4608 x 128 keys: 44 us, the tensor-core kernel takes 66 for any
+// number up to 128; with two rows and 24 heads of 512 keys it is ahead, 9.8 to
+// 14.4 us), with fp32 up to sixteen (521 us for 80 heads of 4608 x 128 keys, the
+// tiled kernel 894).
+// It has eight CTAs a key head at most, so long keys of few heads stay with the
+// tensor-core kernel's shares (one head of 32768 keys: 25 us, here 50).
+bool cross_few_rows(const CrossShape& s) {
+  const long long rows = (long long)(s.heads / s.kv_heads) * s.Lq;
+  if (s.dtype == PISA_FP32) return rows <= 16;
+  return rows == 1 && (s.Lk <= 8 * 2048 || 2 * s.batch * s.kv_heads >= kSMs);
+}
+
 struct CrossFwdPlan {
   CrossPackPlan pack;
   int splits;
   size_t part, part_lse, total;
 };
 
-// Tensor-core forward: shares of the keys where the pairs of query tiles leave
-// at least half of the SMs without work (each share re-reads its query tiles
-// and its output goes through memory in 32 bits, which a few rows can afford).
+// Tensor-core forward: shares of a head's key tiles.  The time follows the
+// waves of CTAs (one per SM) times the steps of one, of which about two go to
+// its start and end; joining the shares costs a launch (about two steps) and
+// takes their outputs through memory in 32 bits (one step: about 8 MB), so it
+// pays where there are few rows and long keys: 80 heads of one tile of rows and
+// 36 of keys, 66 us without shares.
 CrossFwdPlan cross_fwd_plan(const CrossShape& s) {
   CrossFwdPlan p{};
   p.splits = 1;
-  if (s.dtype == PISA_BF16) {
+  if (s.dtype == PISA_BF16 && !cross_few_rows(s)) {
     p.pack = cross_pack_plan(s, false);
     const long long items = (long long)s.batch * s.heads * (((s.Lq + 127) / 128 + 1) / 2), tiles = (s.Lk + 127) / 128;
-    if (2 * items <= kSMs && tiles > 1) p.splits = (int)(kSMs / items < tiles ? kSMs / items : tiles);
+    const double step_bytes = 8e6, out = 8.0 * s.batch * s.heads * s.Lq * s.d;  // written and read
+    double best = 0.0;
+    for (int n = 1; n <= tiles && n <= 32 && (n == 1 || items * n <= 4 * kSMs); ++n) {
+      const double waves = (double)((items * n + kSMs - 1) / kSMs);
+      const double cost = waves * ((tiles + n - 1) / n + 2) + (n > 1 ? 2.0 + n * out / step_bytes : 0.0);
+      if (n == 1 || cost < best) {
+        best = cost;
+        p.splits = n;
+      }
+    }
     if (p.splits > 1) {
       const size_t rows = (size_t)p.splits * s.batch * s.heads * s.Lq;
       p.part = align_up(rows * s.d * sizeof(float));
@@ -200,7 +227,6 @@ CrossFwdPlan cross_fwd_plan(const CrossShape& s) {
     }
   }
   p.total = p.pack.total + p.part + p.part_lse;
-  if (p.total < 16) p.total = 16;
   return p;
 }
 
@@ -361,9 +387,58 @@ pisa_status run_cross_fwd_sm100(const CrossArgs& a, const CrossShape& s, char* w
   return last_launch();
 }
 
+// CTAs of a cluster, 1 to 8: the time follows the number of waves of resident
+// CTAs times what one takes, its keys and a start and an end that are worth
+// about 768 keys (80 heads of 4608 x 128 keys: 44 us with 3 CTAs a head in one
+// wave, 58 us with 7 in two).
+constexpr int kRowsFixed = 768;
+
+template <typename T, int D, int NQ>
+pisa_status launch_cross_rows(const CrossArgs& a, const CrossShape& s, cudaStream_t st) {
+  const int rows = s.heads / s.kv_heads * s.Lq, z = (rows + NQ - 1) / NQ, y = s.batch * s.kv_heads;
+  constexpr size_t ring = cross_rows_bytes<T, D>();
+  // always: with the kernel's static part 48 KB of ring are past the default limit
+  if (cudaFuncSetAttribute(cross_rows_kernel<T, D, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ring) !=
+      cudaSuccess)
+    return PISA_ERR_CUDA;
+  static const int per_sm = [] {
+    int n = 0;
+    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, cross_rows_kernel<T, D, NQ>, kRowsThreads, ring) ==
+                   cudaSuccess && n > 0
+               ? n
+               : 1;
+  }();
+  const long long slots = (long long)kSMs * per_sm;
+  int x = 1;
+  long long best = -1;
+  for (int c = 1; c <= kRowsCluster; ++c) {
+    const long long waves = ((long long)y * z * c + slots - 1) / slots, cost = waves * ((s.Lk + c - 1) / c + kRowsFixed);
+    if (best < 0 || cost < best) {
+      best = cost;
+      x = c;
+    }
+  }
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)x;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)x, y, z);
+  cfg.blockDim = dim3(kRowsThreads);
+  cfg.dynamicSmemBytes = ring;
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, cross_rows_kernel<T, D, NQ>, a) == cudaSuccess ? PISA_OK : PISA_ERR_CUDA;
+}
+
 template <typename T, int D>
 struct CrossFwdOp {
   static pisa_status run(const CrossArgs& a, const CrossShape& s, char* ws, cudaStream_t st) {
+    if (cross_few_rows(s))
+      return std::is_same<T, __nv_bfloat16>::value || s.heads / s.kv_heads * s.Lq == 1
+                 ? launch_cross_rows<T, D, 1>(a, s, st)
+                 : launch_cross_rows<float, D, 2>(a, s, st);
     if constexpr (std::is_same<T, __nv_bfloat16>::value) {
       return run_cross_fwd_sm100<D>(a, s, ws, st);
     } else {
@@ -466,7 +541,8 @@ pisa_status cross_fwd_api(const void* q, const void* k, const void* v, void* out
   HeadView w[4];
   if (!cross_tensors_ok(s, ptr, "qkkq", 4, strides, w)) return PISA_ERR_INVALID_ARG;
   if (!aligned_to(lse, 4) || !aligned_to(kv_len, 4)) return PISA_ERR_INVALID_ARG;
-  if (ws == nullptr || ws_bytes < cross_fwd_plan(s).total) return PISA_ERR_WORKSPACE;
+  const size_t need = cross_fwd_plan(s).total;
+  if (need > 0 && (ws == nullptr || ws_bytes < need)) return PISA_ERR_WORKSPACE;
   if (!aligned16(ws)) return PISA_ERR_INVALID_ARG;
   CrossArgs a = cross_args(s, kv_len, key_mask);
   a.q = q;

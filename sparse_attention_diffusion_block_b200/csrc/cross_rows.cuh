@@ -1,0 +1,261 @@
+// Cross-attention of a few query rows (a single token, a handful of learned
+// queries) to many keys.  The formulas are those at the head of
+// cross_simt.cuh.
+//
+// Bound by reading the keys and values once, so nothing here wants a tensor
+// core: a 128-row MMA tile would be nearly empty.  A cluster of up to eight
+// CTAs shares the keys of one key head; the four lanes of a group hold one key
+// at a time (each a quarter of its elements, in 16-byte pieces of whole 64-byte
+// segments), and every group keeps its own running maximum, sum and output, so
+// that the keys of a warp never wait for one another.  Keys and values come
+// through three stages of shared memory by cp.async, two of them always under
+// way (loads into registers kept 64 KB an SM in flight half of the time: 56 us
+// for 80 heads of 4608 x 128 keys); a lane reads back only what it copied, so
+// no barrier is needed.  They are
+// joined once at the end: lanes by shuffles, warps through shared memory, CTAs
+// through distributed shared memory; one launch, no workspace, no atomics.
+// Rows of the query heads that share the key head are taken together, NQ at a
+// time.
+#pragma once
+
+#include <cooperative_groups.h>
+
+#include "cross_simt.cuh"
+
+namespace pisa {
+
+constexpr int kRowsCluster = 8;  // most CTAs of a cluster
+constexpr int kRowsThreads = 256, kRowsWarps = kRowsThreads / 32;
+
+constexpr int kRowsStages = 3;
+
+template <typename T, int D>
+constexpr size_t cross_rows_bytes() {  // stages x threads x (key, value) pieces
+  return (size_t)kRowsStages * kRowsThreads * 2 * (D / 4 * sizeof(T));
+}
+
+__device__ __forceinline__ void cp_async16(void* dst, const void* src, bool on) {
+  const int bytes = on ? 16 : 0;  // the rest is filled with zeros
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                   static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+               "l"(src), "r"(bytes)
+               : "memory");
+}
+
+// Two packed 32-bit fused multiply-adds.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)),
+        "l"(*reinterpret_cast<const uint64_t*>(&c)));
+  return *reinterpret_cast<const float2*>(&d);
+}
+
+// The elements of a 16-byte piece as pairs.
+__device__ __forceinline__ float2 piece_pair(const uint4& raw, int i, float) {
+  return reinterpret_cast<const float2*>(&raw)[i];
+}
+__device__ __forceinline__ float2 piece_pair(const uint4& raw, int i, __nv_bfloat16) {
+  return __bfloat1622float2(reinterpret_cast<const __nv_bfloat162*>(&raw)[i]);
+}
+
+template <int D, int NQ>
+struct CrossRowsShared {
+  float o[kRowsWarps][NQ][D];
+  float m[kRowsWarps][NQ], l[kRowsWarps][NQ];
+  float co[NQ][D];  // this CTA's share
+  float cm[NQ], cl[NQ];
+};
+
+// Grid: (cluster CTAs, batch * kv_heads, groups of NQ rows).
+template <typename T, int D, int NQ>
+__global__ void __launch_bounds__(kRowsThreads, NQ * D * (int)sizeof(T) <= 256 ? 2 : 1) cross_rows_kernel(const CrossArgs a) {
+  namespace cg = cooperative_groups;
+  constexpr int V = 16 / sizeof(T);         // elements of a load
+  constexpr int NV = D / 4 / V;             // loads of a lane per row
+  constexpr int E = D / 4;                  // elements of a lane
+  __shared__ __align__(16) CrossRowsShared<D, NQ> sh;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, part = lane % 4, key = lane / 4;
+  const int b = blockIdx.y / a.kv_heads, hk = blockIdx.y % a.kv_heads, group = a.heads / a.kv_heads;
+  const int n_rows = group * a.Lq, row0 = blockIdx.z * NQ;
+  const int len = cross_len(a, b);
+  // element i of a lane: load i / V, at part * V + (i / V) * 4 V
+  auto col = [&](int i) { return part * V + i * 4 * V; };
+  float2 q[NQ][E / 2], o[NQ][E / 2];
+  float m[NQ], l[NQ];
+#pragma unroll
+  for (int r = 0; r < NQ; ++r) {
+    const int row = min(row0 + r, n_rows - 1), h = hk * group + row / a.Lq;
+    const T* p = static_cast<const T*>(a.q) + b * a.sq.b + h * a.sq.h + (int64_t)(row % a.Lq) * a.sq.r;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const uint4 raw = *reinterpret_cast<const uint4*>(p + col(i));
+#pragma unroll
+      for (int j = 0; j < V / 2; ++j) {
+        const float2 y = piece_pair(raw, j, T());
+        q[r][i * V / 2 + j] = make_float2(y.x * (a.scale * kLog2e), y.y * (a.scale * kLog2e));
+      }
+    }
+    m[r] = -INFINITY;
+    l[r] = 0.f;
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) o[r][i] = make_float2(0.f, 0.f);
+  }
+  const T* k = static_cast<const T*>(a.k) + b * a.sk.b + hk * a.sk.h;
+  const T* v = static_cast<const T*>(a.v) + b * a.sv.b + hk * a.sv.h;
+  const int stride = gridDim.x * kRowsWarps * 8;
+  extern __shared__ __align__(16) uint8_t ring[];  // [stage][warp][key, value][piece][lane] of 16 bytes
+  auto slot = [&](int s, int kv, int i) {
+    return reinterpret_cast<uint4*>(ring) + (((s * kRowsWarps + warp) * 2 + kv) * NV + i) * 32 + lane;
+  };
+  const int first = (blockIdx.x * kRowsWarps + warp) * 8;
+  const int n = first < len ? (len - first + stride - 1) / stride : 0;  // the same for the whole warp
+  unsigned ons = 0;  // bit s: the key in stage s is allowed
+  const T* kp = k + (first + key) * a.sk.r + col(0);
+  const T* vp = v + (first + key) * a.sv.r + col(0);
+  const int64_t k_step = stride * a.sk.r, v_step = stride * a.sv.r;
+  auto load = [&](int it) {
+    if (it < n) {
+      const int s = it % kRowsStages;
+      const bool on = cross_allowed(a, b, len, first + it * stride + key);
+      ons = (ons & ~(1u << s)) | ((on ? 1u : 0u) << s);
+      const T* kq = on ? kp : k;  // nothing is read of the others
+      const T* vq = on ? vp : v;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        cp_async16(slot(s, 0, i), kq + i * 4 * V, on);
+        cp_async16(slot(s, 1, i), vq + i * 4 * V, on);
+      }
+      kp += k_step;
+      vp += v_step;
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int it = 0; it < kRowsStages - 1; ++it) load(it);
+  for (int it = 0; it < n; ++it) {
+    load(it + kRowsStages - 1);
+    asm volatile("cp.async.wait_group %0;" ::"n"(kRowsStages - 1) : "memory");
+    const int st = it % kRowsStages;
+    const bool on = (ons >> st) & 1u;
+    float2 x2[NQ][2];
+#pragma unroll
+    for (int r = 0; r < NQ; ++r) x2[r][0] = x2[r][1] = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const uint4 raw = *slot(st, 0, i);
+#pragma unroll
+      for (int c = 0; c < V / 2; ++c) {
+        const float2 y = piece_pair(raw, c, T());
+#pragma unroll
+        for (int r = 0; r < NQ; ++r) x2[r][c & 1] = fma2(q[r][i * V / 2 + c], y, x2[r][c & 1]);
+      }
+    }
+    float p[NQ];
+#pragma unroll
+    for (int r = 0; r < NQ; ++r) {
+      float x = (x2[r][0].x + x2[r][0].y) + (x2[r][1].x + x2[r][1].y);
+      x += __shfl_xor_sync(0xffffffffu, x, 1);
+      x += __shfl_xor_sync(0xffffffffu, x, 2);
+      if (!on) x = -INFINITY;
+      // O and l are rescaled only when the maximum grows by more than 8 binary
+      // units (exact: both carry the same factor)
+      if (x > m[r] + 8.f) {
+        const float f = exp2f(m[r] - x);
+        l[r] *= f;
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) o[r][i] = make_float2(o[r][i].x * f, o[r][i].y * f);
+        m[r] = x;
+      }
+      p[r] = on ? exp2f(x - (m[r] == -INFINITY ? 0.f : m[r])) : 0.f;
+      l[r] += p[r];
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const uint4 raw = *slot(st, 1, i);
+#pragma unroll
+      for (int c = 0; c < V / 2; ++c) {
+        const float2 y = piece_pair(raw, c, T());
+#pragma unroll
+        for (int r = 0; r < NQ; ++r) o[r][i * V / 2 + c] = fma2(make_float2(p[r], p[r]), y, o[r][i * V / 2 + c]);
+      }
+    }
+  }
+  // the eight groups of a warp
+#pragma unroll
+  for (int r = 0; r < NQ; ++r) {
+    float top = m[r];
+#pragma unroll
+    for (int s = 4; s < 32; s <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+    const float f = m[r] == -INFINITY ? 0.f : exp2f(m[r] - top);
+    l[r] *= f;
+#pragma unroll
+    for (int s = 4; s < 32; s <<= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], s);
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const float z = i % 2 ? o[r][i / 2].y : o[r][i / 2].x;
+      float y = m[r] == -INFINITY ? 0.f : z * f;
+#pragma unroll
+      for (int s = 4; s < 32; s <<= 1) y += __shfl_xor_sync(0xffffffffu, y, s);
+      if (key == 0) sh.o[warp][r][col(i / V) + i % V] = y;
+    }
+    if (lane == 0) {
+      sh.m[warp][r] = top;
+      sh.l[warp][r] = l[r];
+    }
+  }
+  __syncthreads();
+  // the warps of a CTA
+  for (int e = threadIdx.x; e < NQ * D; e += kRowsThreads) {
+    const int r = e / D, c = e % D;
+    float top = -INFINITY, sum = 0.f, y = 0.f;
+#pragma unroll
+    for (int w = 0; w < kRowsWarps; ++w) top = fmaxf(top, sh.m[w][r]);
+#pragma unroll
+    for (int w = 0; w < kRowsWarps; ++w) {
+      const float f = sh.m[w][r] == -INFINITY ? 0.f : exp2f(sh.m[w][r] - top);
+      sum += f * sh.l[w][r];
+      y += f * sh.o[w][r][c];
+    }
+    sh.co[r][c] = y;
+    if (c == 0) {
+      sh.cm[r] = top;
+      sh.cl[r] = sum;
+    }
+  }
+  // the CTAs of the cluster: each joins its share of the elements
+  const cg::cluster_group cluster = cg::this_cluster();
+  cluster.sync();
+  const int ctas = gridDim.x;
+  for (int e = blockIdx.x * kRowsThreads + threadIdx.x; e < NQ * D; e += ctas * kRowsThreads) {
+    const int r = e / D, c = e % D, row = row0 + r;
+    // all remote reads at once: each takes most of a microsecond
+    float cm[kRowsCluster], cl[kRowsCluster], co[kRowsCluster];
+#pragma unroll
+    for (int s = 0; s < kRowsCluster; ++s) {
+      const CrossRowsShared<D, NQ>* p = cluster.map_shared_rank(&sh, s < ctas ? s : 0);
+      cm[s] = p->cm[r];
+      cl[s] = p->cl[r];
+      co[s] = p->co[r][c];
+    }
+    float top = -INFINITY, sum = 0.f, y = 0.f;
+#pragma unroll
+    for (int s = 0; s < kRowsCluster; ++s) top = s < ctas ? fmaxf(top, cm[s]) : top;
+#pragma unroll
+    for (int s = 0; s < kRowsCluster; ++s) {
+      const float f = s >= ctas || cm[s] == -INFINITY ? 0.f : exp2f(cm[s] - top);
+      sum += s < ctas ? f * cl[s] : 0.f;
+      y += s < ctas ? f * co[s] : 0.f;
+    }
+    if (row >= n_rows) continue;
+    const int h = hk * group + row / a.Lq, i = row % a.Lq;
+    T* out = static_cast<T*>(a.out) + b * a.so.b + h * a.so.h + (int64_t)i * a.so.r + c;
+    *out = from_float<T>(sum == 0.f ? 0.f : y / sum);
+    if (a.lse != nullptr && c == 0)
+      a.lse[((int64_t)b * a.heads + h) * a.Lq + i] = (top + log2f(sum)) * 0.6931471805599453f;
+  }
+  cluster.sync();  // no CTA leaves while another reads its shared memory
+}
+
+}  // namespace pisa

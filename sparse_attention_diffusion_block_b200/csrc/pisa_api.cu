@@ -13,6 +13,7 @@
 
 #include "common.cuh"
 #include "cross_bwd_sm100.cuh"
+#include "cross_rows.cuh"
 #include "cross_simt.cuh"
 #include "cross_sm100.cuh"
 #include "fused_simt.cuh"
@@ -1109,7 +1110,8 @@ size_t pisa_cross_workspace_size(pisa_dtype dtype, int batch, int heads, int kv_
                                  int masked, int backward) {
   const CrossShape s{dtype, batch, heads, kv_heads, Lq, Lk, d, masked != 0};
   if (check_cross(s) != PISA_OK) return 0;
-  return backward ? cross_bwd_plan(s).total : cross_fwd_plan(s).total;
+  const size_t need = backward ? cross_bwd_plan(s).total : cross_fwd_plan(s).total;
+  return need < 16 ? 16 : need;
 }
 
 pisa_status pisa_cross_attn_fwd(const void* q, const void* k, const void* v, void* out, float* lse,

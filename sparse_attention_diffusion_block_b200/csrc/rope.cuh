@@ -10,11 +10,13 @@
 // and more, where a 32-bit angle has lost two decimals); the reduced angle,
 // its sine and cosine and the rotation are 32-bit; one rounding at the store.
 //
-// Bound by HBM: each element is read and written once.  One thread keeps the
-// sine and cosine of its pairs in registers and walks over the heads, so the
-// angles (about 100 instructions a pair, 64-bit ones among them) are paid once
-// per token and head group, not per row, and there is no table to read.
+// Bound by HBM: each element is read and written once.  The angles (about 100
+// instructions a pair, 64-bit ones among them) are formed once per token, in
+// shared memory; a thread keeps the sines and cosines of its pairs in registers
+// and walks over the heads.  There is no table in memory to read.
 #pragma once
+
+#include <type_traits>
 
 #include "common.cuh"
 
@@ -34,44 +36,35 @@ struct RopeArgs {
   RopeTensor q, k;
   const float* pos;
   int64_t pos_batch;  // elements between the positions of two batch entries (0: shared)
-  int L, d, axes, pairs;
+  int L, d, axes, pairs, tokens;
   float sign, magnitude;
   double freq[kRopeMaxPairs];
   unsigned char axis[kRopeMaxPairs];
 };
 
-// V consecutive elements as floats: whole 16-byte words when V x sizeof(T) is
-// a multiple of 16, element by element otherwise.
+// V consecutive elements as floats, in accesses of 16 or 8 bytes where V
+// elements are that long, element by element otherwise.
 template <typename T, int V>
-__device__ __forceinline__ void rope_load(const T* p, float* x) {
-  if constexpr (sizeof(T) * V % 16 == 0) {
-    constexpr int W = sizeof(T) * V / 16;
-    uint4 raw[W];
+struct RopeRun {
+  using Word = std::conditional_t<sizeof(T) * V % 16 == 0, uint4, std::conditional_t<sizeof(T) * V == 8, uint2, T>>;
+  static constexpr int N = sizeof(T) * V / sizeof(Word);
+  static __device__ __forceinline__ void load(const T* p, float* x) {
+    Word raw[N];
 #pragma unroll
-    for (int w = 0; w < W; ++w) raw[w] = reinterpret_cast<const uint4*>(p)[w];
+    for (int w = 0; w < N; ++w) raw[w] = reinterpret_cast<const Word*>(p)[w];
     const T* e = reinterpret_cast<const T*>(raw);
 #pragma unroll
     for (int i = 0; i < V; ++i) x[i] = to_float(e[i]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; ++i) x[i] = to_float(p[i]);
   }
-}
-template <typename T, int V>
-__device__ __forceinline__ void rope_store(T* p, const float* x) {
-  if constexpr (sizeof(T) * V % 16 == 0) {
-    constexpr int W = sizeof(T) * V / 16;
-    uint4 raw[W];
+  static __device__ __forceinline__ void store(T* p, const float* x) {
+    Word raw[N];
     T* e = reinterpret_cast<T*>(raw);
 #pragma unroll
     for (int i = 0; i < V; ++i) e[i] = from_float<T>(x[i]);
 #pragma unroll
-    for (int w = 0; w < W; ++w) reinterpret_cast<uint4*>(p)[w] = raw[w];
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; ++i) p[i] = from_float<T>(x[i]);
+    for (int w = 0; w < N; ++w) reinterpret_cast<Word*>(p)[w] = raw[w];
   }
-}
+};
 
 __device__ __forceinline__ void rope_angle(double pos, double freq, float* s, float* c) {
   constexpr double kTwoPi = 6.283185307179586476925;
@@ -82,67 +75,66 @@ __device__ __forceinline__ void rope_angle(double pos, double freq, float* s, fl
   sincosf((float)r, s, c);
 }
 
-// A thread owns one unit of a token's row: V elements (interleaved) or V
-// pairs, i.e. two runs of V elements (half; copied units beyond the rotated
-// part are two adjacent runs).  Blocks: x tokens, y head groups, z batch.
+// A block takes `tokens` tokens (a power of two) of all heads: it forms their
+// angles once, into shared memory, and then its threads walk over the rows.  A
+// thread owns one unit of a row: V elements (interleaved) or V pairs, i.e. two
+// runs of V elements (half; copied units beyond the turned part are two
+// adjacent runs).  Grid: (token groups, batch).
 template <typename T, bool HALF, int V>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int NP = HALF ? V : V / 2;  // pairs of a unit
   constexpr int R = HALF ? 2 : 1;       // runs of V elements of a unit
-  const int units = a.d / (R * V);
-  const int tokens = kRopeThreads / units;
-  const int unit = threadIdx.x % units;
-  const int t = blockIdx.x * tokens + threadIdx.x / units;
-  if (threadIdx.x >= tokens * units || t >= a.L) return;
-  const int b = blockIdx.z;
+  extern __shared__ float2 rope_turns[];  // [tokens][pairs]: (cos, sin), magnitude and sign included
+  const int b = blockIdx.y, t0 = blockIdx.x * a.tokens;
+  const int here = min(a.tokens, a.L - t0);
+  const float* pos = a.pos + b * a.pos_batch + (int64_t)t0 * a.axes;
+  for (int e = threadIdx.x; e < here * a.pairs; e += kRopeThreads) {
+    const int p = e % a.pairs;
+    float s, c;
+    rope_angle((double)pos[e / a.pairs * a.axes + a.axis[p]], a.freq[p], &s, &c);
+    rope_turns[e] = make_float2(c * a.magnitude, s * a.sign * a.magnitude);
+  }
+  __syncthreads();
+  const int units = a.d / (R * V), unit = threadIdx.x % units, slot = threadIdx.x / units;
+  const int tok = slot % a.tokens, t = t0 + tok;
+  if (tok >= here) return;
   const bool turn = unit * NP < a.pairs;
   float s[NP], c[NP];
   if (turn) {
-    const float* pos = a.pos + b * a.pos_batch + (int64_t)t * a.axes;
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-      const int p = unit * NP + i;
-      rope_angle((double)pos[a.axis[p]], a.freq[p], &s[i], &c[i]);
-      s[i] *= a.sign * a.magnitude;
-      c[i] *= a.magnitude;
+      const float2 cs = rope_turns[tok * a.pairs + unit * NP + i];
+      c[i] = cs.x;
+      s[i] = cs.y;
     }
   }
   const int e0 = HALF ? (turn ? unit * V : 2 * a.pairs + (unit * V - a.pairs) * 2) : unit * V;
   const int e1 = e0 + (turn ? a.pairs : V);  // second run (half layout)
-  const int rows = a.q.heads + a.k.heads;
-  constexpr int U = 4;  // rows in flight
-  for (int h0 = blockIdx.y; h0 < rows; h0 += U * gridDim.y) {
-    float x[U][R * V];
+  const int rows = a.q.heads + a.k.heads, step = kRopeThreads / units / a.tokens;
+  // One row at a time: few registers, so that 2048 threads an SM are there to
+  // hide the loads (75600 tokens, 2 x 40 heads of 128: 507 us; two rows in
+  // flight 575, four 660).
+  for (int h = slot / a.tokens; h < rows; h += step) {
+    const bool is_q = h < a.q.heads;
+    const RopeTensor& y = is_q ? a.q : a.k;
+    const int hh = is_q ? h : h - a.q.heads;
+    const T* p = static_cast<const T*>(y.in) + b * y.ib + (int64_t)hh * y.ih + t * y.il;
+    float x[R * V];
+    RopeRun<T, V>::load(p + e0, x);
+    if (HALF) RopeRun<T, V>::load(p + e1, x + V);
+    if (turn) {
 #pragma unroll
-    for (int j = 0; j < U; ++j) {
-      const int h = h0 + j * (int)gridDim.y;
-      if (h >= rows) continue;
-      const bool is_q = h < a.q.heads;
-      const RopeTensor& y = is_q ? a.q : a.k;
-      const T* p = static_cast<const T*>(y.in) + b * y.ib + (int64_t)(is_q ? h : h - a.q.heads) * y.ih + t * y.il;
-      rope_load<T, V>(p + e0, x[j]);
-      if (HALF) rope_load<T, V>(p + e1, x[j] + V);
-    }
-#pragma unroll
-    for (int j = 0; j < U; ++j) {
-      const int h = h0 + j * (int)gridDim.y;
-      if (h >= rows) continue;
-      if (turn) {
-#pragma unroll
-        for (int i = 0; i < NP; ++i) {
-          float& u = x[j][HALF ? i : 2 * i];
-          float& w = x[j][HALF ? V + i : 2 * i + 1];
-          const float u0 = u, w0 = w;
-          u = u0 * c[i] - w0 * s[i];
-          w = u0 * s[i] + w0 * c[i];
-        }
+      for (int i = 0; i < NP; ++i) {
+        float& u = x[HALF ? i : 2 * i];
+        float& w = x[HALF ? V + i : 2 * i + 1];
+        const float u0 = u, w0 = w;
+        u = u0 * c[i] - w0 * s[i];
+        w = u0 * s[i] + w0 * c[i];
       }
-      const bool is_q = h < a.q.heads;
-      const RopeTensor& y = is_q ? a.q : a.k;
-      T* p = static_cast<T*>(y.out) + b * y.ob + (int64_t)(is_q ? h : h - a.q.heads) * y.oh + t * y.ol;
-      rope_store<T, V>(p + e0, x[j]);
-      if (HALF) rope_store<T, V>(p + e1, x[j] + V);
     }
+    T* o = static_cast<T*>(y.out) + b * y.ob + (int64_t)hh * y.oh + t * y.ol;
+    RopeRun<T, V>::store(o + e0, x);
+    if (HALF) RopeRun<T, V>::store(o + e1, x + V);
   }
 }
 

@@ -131,8 +131,8 @@ def test_cross_refuses(lib):
         assert call(d=80) == lib.PISA_ERR_UNSUPPORTED
         assert call(b=300, h=300, hk=300) == lib.PISA_ERR_UNSUPPORTED
         assert call(Lq=(1 << 30) + 1) == lib.PISA_ERR_UNSUPPORTED
-        assert call(ws=None) == lib.PISA_ERR_WORKSPACE
-        assert call(n=8) == lib.PISA_ERR_WORKSPACE
+        assert call(ws=None, kv_len=FAKE) == lib.PISA_ERR_WORKSPACE
+        assert call(n=8, mask=FAKE) == lib.PISA_ERR_WORKSPACE
         rows, keys = (25600, 6400, 64), (6400, 3200, 64)
         order = [rows, keys, keys, rows] if call is fwd else [rows, rows, keys, keys, rows, rows, keys, keys]
         for i in range(len(order)):

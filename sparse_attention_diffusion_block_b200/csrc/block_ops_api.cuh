@@ -192,6 +192,20 @@ bool cross_few_rows(const CrossShape& s) {
   return rows == 1 && (s.Lk <= 8 * 2048 || 2 * s.batch * s.kv_heads >= kSMs);
 }
 
+// CUDA-core kernels with query rows per CTA: 64, or 16 where 64 would leave SMs
+// without work (1024 x 77: one head 9.3 us with 16 rows, 13.7 with 64; eight
+// heads 25.6 and 14.3).  Shares of the
+// keys, at least two tiles each, up to two CTAs per SM.
+int cross_simt_ri(const CrossShape& s) {
+  return 2LL * s.batch * s.heads * ((s.Lq + 63) / 64) >= kSMs ? 4 : 1;
+}
+int cross_simt_splits(const CrossShape& s, int bn) {
+  const int bm = 16 * cross_simt_ri(s);
+  const long long ctas = (long long)s.batch * s.heads * ((s.Lq + bm - 1) / bm);
+  const long long n = 2LL * kSMs / ctas, most = ((s.Lk + bn - 1) / bn) / 2;
+  return (int)(n < most ? (n < 1 ? 1 : n) : (most < 1 ? 1 : most));
+}
+
 struct CrossFwdPlan {
   CrossPackPlan pack;
   int splits;
@@ -220,11 +234,13 @@ CrossFwdPlan cross_fwd_plan(const CrossShape& s) {
         p.splits = n;
       }
     }
-    if (p.splits > 1) {
-      const size_t rows = (size_t)p.splits * s.batch * s.heads * s.Lq;
-      p.part = align_up(rows * s.d * sizeof(float));
-      p.part_lse = align_up(rows * sizeof(float));
-    }
+  } else if (!cross_few_rows(s)) {
+    p.splits = cross_simt_splits(s, 64);
+  }
+  if (p.splits > 1) {
+    const size_t rows = (size_t)p.splits * s.batch * s.heads * s.Lq;
+    p.part = align_up(rows * s.d * sizeof(float));
+    p.part_lse = align_up(rows * sizeof(float));
   }
   p.total = p.pack.total + p.part + p.part_lse;
   return p;
@@ -232,11 +248,12 @@ CrossFwdPlan cross_fwd_plan(const CrossShape& s) {
 
 struct CrossBwdPlan {
   CrossPackPlan pack;
-  int splits;  // CUDA cores: shares of the query tiles; tensor cores: CTAs of the dk/dv kernel
+  int splits;     // dk/dv: CUDA cores, shares of the query tiles; tensor cores, CTAs
+  int dq_splits;  // CUDA cores: shares of the keys
   size_t delta, part, total;
 };
 
-// fp32: query shares per key tile, enough CTAs for two per SM, at least eight
+// fp32: query shares per key tile, enough CTAs for two per SM, at least two
 // query tiles each, and partials of at most 256 MB.  bf16: one CTA per SM, but
 // at least eight steps of 64 query rows each.
 CrossBwdPlan cross_bwd_plan(const CrossShape& s) {
@@ -245,18 +262,25 @@ CrossBwdPlan cross_bwd_plan(const CrossShape& s) {
   p.delta = align_up((size_t)s.batch * s.heads * s.Lq * sizeof(float));
   if (s.dtype == PISA_BF16) {
     p.pack = cross_pack_plan(s, true);
-    const long long items = slices * ((s.Lk + 127) / 128), steps = items * group * ((s.Lq + 63) / 64);
-    const long long n = (steps + 7) / 8;
-    p.splits = (int)(n < kSMs ? n : kSMs);
+    // with a mask any number of CTAs, otherwise equal ranges of every key tile's steps
+    const long long tiles = (s.Lk + 127) / 128, items = slices * tiles, steps = slices * group * ((s.Lq + 63) / 64);
+    const long long lanes = s.masked ? 1 : tiles, all = s.masked ? steps * tiles : steps;
+    const long long most = (all + 7) / 8, n = kSMs / lanes < 1 ? 1 : kSMs / lanes;
+    p.splits = (int)(lanes * (n < most ? n : most));
     p.part = align_up((size_t)(items + p.splits) * 2 * 128 * s.d * sizeof(float));
   } else {
-    const long long ctas = slices * ((s.Lk + 63) / 64), tiles = group * ((s.Lq + 31) / 32);
+    const int bq = s.d == 64 ? 64 : 32;
+    const long long ctas = slices * ((s.Lk + 63) / 64), tiles = group * ((s.Lq + bq - 1) / bq);
     const long long one = 2LL * slices * s.Lk * s.d * sizeof(float);
     long long n = (2LL * kSMs + ctas - 1) / ctas;
-    if (n > tiles / 8) n = tiles / 8;
+    if (n > tiles / 2) n = tiles / 2;
     if (n > (256LL << 20) / one) n = (256LL << 20) / one;
     p.splits = (int)(n < 1 ? 1 : n);
-    p.part = p.splits > 1 ? align_up((size_t)p.splits * one) : 0;
+    p.dq_splits = cross_simt_splits(s, bq);
+    // the two kernels' partials, one after the other in the same place
+    const size_t kv = p.splits > 1 ? (size_t)p.splits * one : 0;
+    const size_t dq = p.dq_splits > 1 ? (size_t)p.dq_splits * s.batch * s.heads * s.Lq * s.d * sizeof(float) : 0;
+    p.part = align_up(kv > dq ? kv : dq);
   }
   p.total = p.pack.total + p.delta + p.part;
   return p;
@@ -359,6 +383,16 @@ CrossFwdArgs cross_work(const CrossShape& s, const int32_t* count, int splits) {
   return f;
 }
 
+template <typename T, int D>
+pisa_status launch_cross_join(const CrossArgs& a, const CrossShape& s, int splits, const float* part,
+                              const float* part_lse, cudaStream_t st) {
+  const int64_t rows = (int64_t)s.batch * s.heads * s.Lq;
+  constexpr int per = 256 / (D / 4);
+  const CrossJoinArgs j{part, part_lse, a.out, a.so, a.lse, rows, s.heads, s.Lq, splits};
+  cross_join_kernel<T, D><<<(unsigned)((rows + per - 1) / per), 256, 0, st>>>(j);
+  return last_launch();
+}
+
 template <int D>
 pisa_status run_cross_fwd_sm100(const CrossArgs& a, const CrossShape& s, char* ws, cudaStream_t st) {
   const CrossFwdPlan p = cross_fwd_plan(s);
@@ -369,8 +403,6 @@ pisa_status run_cross_fwd_sm100(const CrossArgs& a, const CrossShape& s, char* w
       !make_map_view(&mO, a.out, D, s.Lq, s.heads, s.batch, a.so, 32) || !cross_key_maps<D>(x, 128, &mK, &mV))
     return PISA_ERR_CUDA;
   CrossFwdArgs f = cross_work(s, x.count, p.splits);
-  f.out = static_cast<__nv_bfloat16*>(a.out);
-  f.so = a.so;
   f.lse = a.lse;
   f.part = reinterpret_cast<float*>(ws + p.pack.total);
   f.part_lse = reinterpret_cast<float*>(ws + p.pack.total + p.part);
@@ -381,10 +413,28 @@ pisa_status run_cross_fwd_sm100(const CrossArgs& a, const CrossShape& s, char* w
   if (!regs || !set_smem(cross_fwd_sm100_kernel<D>, smem)) return PISA_ERR_CUDA;
   cross_fwd_sm100_kernel<D><<<f.n_items < sms ? f.n_items : sms, kCrossFwdThreads, smem, st>>>(mQ, mK, mV, mO, f);
   if (last_launch() != PISA_OK || p.splits == 1) return last_launch();
-  constexpr int rows = 256 / (D / 4);
-  const long long n = ((long long)f.BH * s.Lq + rows - 1) / rows;
-  cross_join_kernel<D><<<(unsigned)n, 256, 0, st>>>(f);
+  return launch_cross_join<__nv_bfloat16, D>(a, s, p.splits, f.part, f.part_lse, st);
+}
+
+// Forward on the CUDA cores: RI rows per thread.
+template <int D, int RI>
+pisa_status launch_cross_fwd_simt(const CrossArgs& a, const CrossShape& s, cudaStream_t st) {
+  using L = CrossFwdSimt<D, RI>;
+  if (!set_smem(cross_fwd_simt_kernel<D, RI>, L::bytes())) return PISA_ERR_CUDA;
+  cross_fwd_simt_kernel<D, RI>
+      <<<dim3((s.Lq + L::BM - 1) / L::BM, s.batch * s.heads, a.splits), kCrossThreads, L::bytes(), st>>>(a);
   return last_launch();
+}
+
+template <int D>
+pisa_status run_cross_fwd_simt(CrossArgs a, const CrossShape& s, char* ws, cudaStream_t st) {
+  const CrossFwdPlan p = cross_fwd_plan(s);
+  a.splits = p.splits;
+  a.part = reinterpret_cast<float*>(ws);
+  a.part_lse = reinterpret_cast<float*>(ws + p.part);
+  if (pisa_status e = cross_simt_ri(s) == 4 ? launch_cross_fwd_simt<D, 4>(a, s, st) : launch_cross_fwd_simt<D, 1>(a, s, st))
+    return e;
+  return p.splits == 1 ? PISA_OK : launch_cross_join<float, D>(a, s, p.splits, a.part, a.part_lse, st);
 }
 
 // CTAs of a cluster, 1 to 8: the time follows the number of waves of resident
@@ -439,15 +489,10 @@ struct CrossFwdOp {
       return std::is_same<T, __nv_bfloat16>::value || s.heads / s.kv_heads * s.Lq == 1
                  ? launch_cross_rows<T, D, 1>(a, s, st)
                  : launch_cross_rows<float, D, 2>(a, s, st);
-    if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+    if constexpr (std::is_same<T, __nv_bfloat16>::value)
       return run_cross_fwd_sm100<D>(a, s, ws, st);
-    } else {
-      constexpr int BM = 64;
-      const size_t smem = CrossFwdSimt<D, BM>::bytes();
-      if (!set_smem(cross_fwd_simt_kernel<T, D, BM>, smem)) return PISA_ERR_CUDA;
-      cross_fwd_simt_kernel<T, D, BM><<<dim3((s.Lq + BM - 1) / BM, s.batch * s.heads), kCrossThreads, smem, st>>>(a);
-      return last_launch();
-    }
+    else
+      return run_cross_fwd_simt<D>(a, s, ws, st);
   }
 };
 
@@ -504,22 +549,38 @@ pisa_status run_cross_bwd_sm100(const CrossArgs& a, const CrossShape& s, char* w
   return last_launch();
 }
 
+template <int D, int RI>
+pisa_status launch_cross_dq_simt(const CrossArgs& a, const CrossShape& s, cudaStream_t st) {
+  using L = CrossDqSimt<D, RI>;
+  if (!set_smem(cross_dq_simt_kernel<D, RI>, L::bytes())) return PISA_ERR_CUDA;
+  cross_dq_simt_kernel<D, RI>
+      <<<dim3((s.Lq + L::BM - 1) / L::BM, s.batch * s.heads, a.splits), kCrossThreads, L::bytes(), st>>>(a);
+  return last_launch();
+}
+
 template <int D>
 pisa_status run_cross_bwd_simt(CrossArgs a, const CrossShape& s, char* ws, cudaStream_t st) {
   const CrossBwdPlan p = cross_bwd_plan(s);
-  a.splits = p.splits;
   a.delta = reinterpret_cast<float*>(ws);
   a.part = reinterpret_cast<float*>(ws + p.delta);
-  const size_t s1 = CrossBwdSimt<D>::dq_bytes(), s2 = CrossBwdSimt<D>::dkv_bytes();
-  if (!set_smem(cross_dq_simt_kernel<float, D>, s1) || !set_smem(cross_dkv_simt_kernel<float, D>, s2))
-    return PISA_ERR_CUDA;
-  cross_dq_simt_kernel<float, D><<<dim3((s.Lq + 63) / 64, s.batch * s.heads), kCrossThreads, s1, st>>>(a);
-  if (last_launch() != PISA_OK) return PISA_ERR_CUDA;
-  cross_dkv_simt_kernel<float, D>
-      <<<dim3((s.Lk + 63) / 64, s.batch * s.kv_heads, a.splits), kCrossThreads, s2, st>>>(a);
-  if (last_launch() != PISA_OK || a.splits == 1) return last_launch();
-  const long long n = (long long)s.batch * s.kv_heads * s.Lk * D / 4;
-  cross_dkv_sum_kernel<float, D><<<dim3((unsigned)((n + 255) / 256), 2), 256, 0, st>>>(a);
+  a.splits = p.dq_splits;
+  if (pisa_status e = cross_simt_ri(s) == 4 ? launch_cross_dq_simt<D, 4>(a, s, st) : launch_cross_dq_simt<D, 1>(a, s, st))
+    return e;
+  if (p.dq_splits > 1) {
+    const int64_t rows = (int64_t)s.batch * s.heads * s.Lq;
+    CrossSumArgs c{a.part, rows, rows * D, {static_cast<float*>(a.dq), nullptr}, {a.sdq, a.sdq}, s.heads, s.Lq, p.dq_splits};
+    cross_sum_kernel<D><<<dim3((unsigned)((rows * (D / 4) + 255) / 256), 1), 256, 0, st>>>(c);
+    if (last_launch() != PISA_OK) return PISA_ERR_CUDA;
+  }
+  a.splits = p.splits;
+  constexpr size_t smem = CrossDkvSimt<D>::bytes();
+  if (!set_smem(cross_dkv_simt_kernel<D>, smem)) return PISA_ERR_CUDA;
+  cross_dkv_simt_kernel<D><<<dim3((s.Lk + 63) / 64, s.batch * s.kv_heads, a.splits), kCrossThreads, smem, st>>>(a);
+  if (last_launch() != PISA_OK || p.splits == 1) return last_launch();
+  const int64_t rows = (int64_t)s.batch * s.kv_heads * s.Lk;
+  CrossSumArgs c{a.part, rows, 2 * rows * D, {static_cast<float*>(a.dk), static_cast<float*>(a.dv)}, {a.sdk, a.sdv},
+                 s.kv_heads, s.Lk, p.splits};
+  cross_sum_kernel<D><<<dim3((unsigned)((rows * (D / 4) + 255) / 256), 2), 256, 0, st>>>(c);
   return last_launch();
 }
 

@@ -447,11 +447,17 @@ cross_dq_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
 // TMEM columns: [128x, +64) S^T, [128x + 64, +64) dP^T, [256, +D) dV, [256 + D, +D) dK.
 //
 // Work: the (batch, key head, key tile) items times the steps of all query
-// rows of the heads that read them, laid end to end and cut into equal
-// contiguous ranges, one per CTA: every SM gets the same number of steps
-// whatever the numbers of heads and tiles, and no more than (items + CTAs)
-// pieces exist.  Piece (item i, CTA c) writes its 32-bit sums to slot i + c,
-// and cross_dkv_reduce_kernel adds an item's slots in order.
+// rows of the heads that read them.  It is cut so that every CTA gets the same
+// number of steps whatever the numbers of heads and tiles, and a piece (an item,
+// a run of its steps) writes its 32-bit sums to a slot of its own, which
+// cross_dkv_reduce_kernel adds in order.
+//   Without a mask: CTA c = g tiles + j takes key tile j of every head in range
+// g of the steps of all heads laid end to end, so that the CTAs of one range
+// read the same queries at the same time and all but one of them from L2.  (Cut
+// item by item, 32760 x 512 read its queries four times from HBM, 2.7 GB, and
+// took 0.65 ms.)
+//   With a mask the number of tiles differs from batch entry to batch entry:
+// items one after the other, cut into equal ranges.
 struct CrossDkvArgs {
   const float *lse, *delta;
   const int32_t* count;  // allowed keys per batch entry, or null: Lk
@@ -473,11 +479,12 @@ struct CrossDkvLayout {
   }
 };
 
-// The flat space of (item, step).
+// How the work is cut.
 struct CrossKeySpace {
   int steps, per_head, group;
-  int64_t total;  // steps of all items
-  int64_t n;      // CTAs with work: each has at least one step
+  int lanes;       // key tiles that go side by side (1 with a mask)
+  int64_t heads;   // items of a lane: key heads, with a mask (key head, tile) pairs
+  int64_t ranges;  // of a lane; each has at least one step
   __device__ __forceinline__ static int tiles(const CrossDkvArgs& a, int b) {
     return ((a.count == nullptr ? a.Lk : __ldg(a.count + b)) + 127) / 128;
   }
@@ -485,36 +492,51 @@ struct CrossKeySpace {
     group = a.heads / a.kv_heads;
     per_head = (a.Lq + 63) / 64;
     steps = per_head * group;
-    int64_t items = 0;
-    if (a.count == nullptr)
-      items = (int64_t)a.batch * tiles(a, 0);
-    else
-      for (int b = 0; b < a.batch; ++b) items += tiles(a, b);
-    total = items * a.kv_heads * steps;
-    n = min((int64_t)ctas, (total + 7) / 8);
+    if (a.count == nullptr) {
+      lanes = tiles(a, 0);
+      heads = (int64_t)a.batch * a.kv_heads;
+      ranges = ctas / lanes;
+    } else {
+      lanes = 1;
+      heads = 0;
+      for (int b = 0; b < a.batch; ++b) heads += tiles(a, b);
+      heads *= a.kv_heads;
+      ranges = min((int64_t)ctas, (heads * steps + 7) / 8);
+    }
   }
-  __device__ __forceinline__ int64_t start(int64_t c) const { return c < n ? total * c / n : total; }
-  // the CTA whose range holds position x
-  __device__ __forceinline__ int64_t owner(int64_t x) const { return ((x + 1) * n - 1) / total; }
+  __device__ __forceinline__ int64_t start(int64_t g) const { return g < ranges ? heads * steps * g / ranges : heads * steps; }
+  // the range that holds step x of a lane
+  __device__ __forceinline__ int64_t owner(int64_t x) const { return ((x + 1) * ranges - 1) / (heads * steps); }
+  // where the piece of range g in item `item` of lane j puts its sums: both only
+  // grow along a lane, and one of them does from piece to piece
+  __device__ __forceinline__ int64_t slot(int64_t item, int64_t g, int j) const { return item + g + j * (heads + ranges); }
 };
 
-// A CTA's pieces in order: item `item` = key tile j of (b, hk), steps [u0, u0 + n).
+// A CTA's pieces in order: key tile j of (b, hk), steps [u0, u0 + n).
 struct CrossPiece {
-  int64_t pos, end;
-  int item, b, hk, j, nv, u0, n;
-  int b_items;  // items of the batch entries before b
+  int64_t pos, end, slot;
+  int b, hk, j, nv, u0, n;
+  int b_items;  // with a mask: items of the batch entries before b
   __device__ __forceinline__ CrossPiece(const CrossKeySpace& k) {
-    pos = k.start(blockIdx.x);
-    end = k.start(blockIdx.x + 1);
+    pos = k.start(blockIdx.x / k.lanes);
+    end = k.start(blockIdx.x / k.lanes + 1);
     b = 0;
     b_items = 0;
   }
   __device__ __forceinline__ bool next(const CrossKeySpace& k, const CrossDkvArgs& a) {
     if (pos >= end) return false;
-    item = (int)(pos / k.steps);
+    const int item = (int)(pos / k.steps);
     u0 = (int)(pos % k.steps);
     n = (int)min((int64_t)(k.steps - u0), end - pos);
     pos += n;
+    slot = k.slot(item, blockIdx.x / k.lanes, blockIdx.x % k.lanes);
+    if (a.count == nullptr) {
+      b = item / a.kv_heads;
+      hk = item % a.kv_heads;
+      j = blockIdx.x % k.lanes;
+      nv = a.Lk;
+      return true;
+    }
     int nt = CrossKeySpace::tiles(a, b);
     while (item >= b_items + a.kv_heads * nt) {
       b_items += a.kv_heads * nt;
@@ -522,7 +544,7 @@ struct CrossPiece {
     }
     hk = (item - b_items) / nt;
     j = (item - b_items) % nt;
-    nv = a.count == nullptr ? a.Lk : __ldg(a.count + b);
+    nv = __ldg(a.count + b);
     return true;
   }
 };
@@ -583,9 +605,9 @@ cross_dkv_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
   const CrossKeySpace ks(a, gridDim.x);
   CrossPiece pc(ks);
 
-  // Registers: 2 x 128 x 208 + 128 x 88 = 384 x 168, the launch total.
+  // Registers: 2 x 128 x 200 + 128 x 104 = 384 x 168, the launch total.
   if (warp >= 8) {
-   asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n" ::: "memory");
+   asm volatile("setmaxnreg.dec.sync.aligned.u32 104;\n" ::: "memory");
    if (warp == 8) {
     // ================================================================ producer
     if (lane == 0) {
@@ -687,7 +709,7 @@ cross_dkv_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
     __syncwarp();
    }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;\n" ::: "memory");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;\n" ::: "memory");
     // ================================================================ keys as rows: even steps (warps 0-3), odd (4-7)
     const int x = warp / 4, row = threadIdx.x % 128;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp % 4) * 32) << 16);
@@ -767,7 +789,7 @@ cross_dkv_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       ++pieces;
       fence_after_sync();
       // warps 0-3 write dv, 4-7 dk
-      float* dst = a.part + (((int64_t)pc.item + blockIdx.x) * 2 + x) * 128 * D + row * D;
+      float* dst = a.part + (pc.slot * 2 + x) * 128 * D + row * D;
       const bool in = pc.j * 128 + row < pc.nv;
 #pragma unroll 1
       for (int ch = 0; ch < D / 32; ++ch) {
@@ -814,16 +836,17 @@ __global__ void __launch_bounds__(256) cross_dkv_reduce_kernel(const CrossReduce
   float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
   if (at >= 0) {
     const CrossKeySpace ks(a, r.ctas);
-    int64_t item = 0;
-    if (a.count == nullptr)
-      item = (int64_t)b * CrossKeySpace::tiles(a, 0);
-    else
+    int64_t item = bh;
+    if (a.count != nullptr) {
+      item = 0;
       for (int i = 0; i < b; ++i) item += CrossKeySpace::tiles(a, i);
-    item = item * a.kv_heads + hk * CrossKeySpace::tiles(a, b) + at / 128;
+      item = item * a.kv_heads + hk * CrossKeySpace::tiles(a, b) + at / 128;
+    }
     const int64_t first = ks.owner(item * ks.steps), last = ks.owner((item + 1) * ks.steps - 1);
-    for (int64_t s = first; s <= last; ++s) {
+    const int lane = a.count == nullptr ? at / 128 : 0;
+    for (int64_t g = first; g <= last; ++g) {
       const float4 y = *reinterpret_cast<const float4*>(
-          a.part + (((item + s) * 2 + blockIdx.y) * 128 + at % 128) * D + c);
+          a.part + ((ks.slot(item, g, lane) * 2 + blockIdx.y) * 128 + at % 128) * D + c);
       x.x += y.x;
       x.y += y.y;
       x.z += y.z;

@@ -34,24 +34,6 @@ constexpr size_t cross_rows_bytes() {  // stages x threads x (key, value) pieces
   return (size_t)kRowsStages * kRowsThreads * 2 * (D / 4 * sizeof(T));
 }
 
-__device__ __forceinline__ void cp_async16(void* dst, const void* src, bool on) {
-  const int bytes = on ? 16 : 0;  // the rest is filled with zeros
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                   static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
-               "l"(src), "r"(bytes)
-               : "memory");
-}
-
-// Two packed 32-bit fused multiply-adds.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;"
-      : "=l"(d)
-      : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)),
-        "l"(*reinterpret_cast<const uint64_t*>(&c)));
-  return *reinterpret_cast<const float2*>(&d);
-}
-
 // The elements of a 16-byte piece as pairs.
 __device__ __forceinline__ float2 piece_pair(const uint4& raw, int i, float) {
   return reinterpret_cast<const float2*>(&raw)[i];
@@ -130,13 +112,13 @@ __global__ void __launch_bounds__(kRowsThreads, NQ * D * (int)sizeof(T) <= 256 ?
       kp += k_step;
       vp += v_step;
     }
-    asm volatile("cp.async.commit_group;" ::: "memory");
+    cp_async_commit();
   };
 #pragma unroll
   for (int it = 0; it < kRowsStages - 1; ++it) load(it);
   for (int it = 0; it < n; ++it) {
     load(it + kRowsStages - 1);
-    asm volatile("cp.async.wait_group %0;" ::"n"(kRowsStages - 1) : "memory");
+    cp_async_wait<kRowsStages - 1>();
     const int st = it % kRowsStages;
     const bool on = (ons >> st) & 1u;
     float2 x2[NQ][2];

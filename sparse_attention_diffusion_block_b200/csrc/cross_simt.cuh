@@ -8,8 +8,9 @@
 // dk and dv summed over the query heads that share a key head.
 //
 // fp32 products stay on the CUDA cores: the fp32 tolerance leaves no room for
-// tf32 or bf16 operands.  Bound by the FMA pipe once the tiles fill the GPU.
-// A key that is not allowed is read as a zero row (so whatever its memory
+// tf32 or bf16 operands.  Bound by the FMA pipe and by shared-memory reads once
+// the tiles fill the GPU.  Tiles come by cp.async while the threads work on the
+// ones before; the inner products are packed two to an instruction.  A key that is not allowed is read as a zero row (so whatever its memory
 // holds, NaN included, meets no product), and p and ds of its column are zero.
 // A row without any allowed key gives o = 0, lse = -inf and zero gradients.
 #pragma once
@@ -28,7 +29,8 @@ struct CrossArgs {
   HeadView sq, sk, sv, so, sg, sdq, sdk, sdv;  // so: strides of out (forward) or o (backward)
   float* lse;      // forward: written when not null; backward: read
   float* delta;    // backward: written by the dq kernel, read by the dk/dv kernel
-  float* part;     // backward: partial dk and dv, [splits][2][batch * kv_heads][Lk][d]
+  float* part;     // splits > 1: see each kernel
+  float* part_lse; // forward, splits > 1: [splits][batch * heads][Lq], binary logarithms
   const int32_t* kv_len;
   const uint8_t* key_mask;
   int batch, heads, kv_heads, Lq, Lk, splits;
@@ -44,23 +46,59 @@ __device__ __forceinline__ bool cross_allowed(const CrossArgs& a, int b, int len
 
 constexpr int kCrossThreads = 256;  // 16 x 16 threads
 
+__device__ __forceinline__ void put4(float* p, float a, float b, float c, float d) {
+  *reinterpret_cast<float4*>(p) = make_float4(a, b, c, d);
+}
+__device__ __forceinline__ void put4(__nv_bfloat16* p, float a, float b, float c, float d) {
+  __nv_bfloat162 x[2] = {__floats2bfloat162_rn(a, b), __floats2bfloat162_rn(c, d)};
+  *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(x);
+}
+
+// Two packed 32-bit fused multiply-adds.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)),
+        "l"(*reinterpret_cast<const uint64_t*>(&c)));
+  return *reinterpret_cast<const float2*>(&d);
+}
+
+// 16 bytes to shared memory, or zeros where `on` is false (nothing is read).
+__device__ __forceinline__ void cp_async16(void* dst, const void* src, bool on) {
+  const int bytes = on ? 16 : 0;
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                   static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+               "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // ROWS rows of D floats into shared memory with row pitch D + 4 (a float4
-// column of 16 consecutive rows then covers all banks).  Rows for which
-// `ok(row)` is false become zeros and are not read.
-template <typename T, int D, int ROWS, typename F>
-__device__ __forceinline__ void cross_tile(float* s, const T* base, int64_t pitch, F ok) {
-  for (int e = threadIdx.x; e < ROWS * (D / 8); e += kCrossThreads) {
-    const int r = e / (D / 8), c = (e % (D / 8)) * 8;
-    float x[8] = {};
-    if (ok(r)) load8(base + r * pitch + c, x);
-    *reinterpret_cast<float4*>(s + r * (D + 4) + c) = make_float4(x[0], x[1], x[2], x[3]);
-    *reinterpret_cast<float4*>(s + r * (D + 4) + c + 4) = make_float4(x[4], x[5], x[6], x[7]);
+// column of 16 consecutive rows then covers all banks); zeros for rows that are
+// not ok.  One commit group.
+template <int D, int ROWS, typename F>
+__device__ __forceinline__ void cross_tile(float* s, const float* base, int64_t pitch, F ok) {
+#pragma unroll 2
+  for (int e = threadIdx.x; e < ROWS * (D / 4); e += kCrossThreads) {
+    const int r = e / (D / 4), c = e % (D / 4) * 4;
+    const bool on = ok(r);
+    cp_async16(s + r * (D + 4) + c, on ? base + r * pitch + c : base, on);
   }
 }
 
-// acc[i][j] += a[ty RI + i] . b[tx + 16 j]: RI x NJ dot products of length D.
+// acc[i][j] = a[ty RI + i] . b[tx + 16 j]: RI x NJ dot products of length D.
 template <int D, int RI, int NJ>
-__device__ __forceinline__ void cross_dots(const float* a, const float* b, int ty, int tx, float (&acc)[RI][NJ]) {
+__device__ __forceinline__ void cross_dots(const float* a, const float* b, int ty, int tx, float (&out)[RI][NJ]) {
+  float2 acc[RI][NJ];
+#pragma unroll
+  for (int i = 0; i < RI; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) acc[i][j] = make_float2(0.f, 0.f);
 #pragma unroll 4
   for (int c = 0; c < D; c += 4) {
     float4 x[RI], y[NJ];
@@ -72,18 +110,20 @@ __device__ __forceinline__ void cross_dots(const float* a, const float* b, int t
     for (int i = 0; i < RI; ++i)
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
-        acc[i][j] = fmaf(x[i].x, y[j].x, acc[i][j]);
-        acc[i][j] = fmaf(x[i].y, y[j].y, acc[i][j]);
-        acc[i][j] = fmaf(x[i].z, y[j].z, acc[i][j]);
-        acc[i][j] = fmaf(x[i].w, y[j].w, acc[i][j]);
+        acc[i][j] = fma2(make_float2(x[i].x, x[i].y), make_float2(y[j].x, y[j].y), acc[i][j]);
+        acc[i][j] = fma2(make_float2(x[i].z, x[i].w), make_float2(y[j].z, y[j].w), acc[i][j]);
       }
   }
+#pragma unroll
+  for (int i = 0; i < RI; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) out[i][j] = acc[i][j].x + acc[i][j].y;
 }
 
-// acc[i][.] += sum_n w[ty RI + i][n] m[n][.]: the columns of thread tx are the
-// float4s tx + 16 m of a row of D.  w has row pitch WP, n runs over N.
+// acc[i] += sum_n w[ty RI + i][n] m[n]: the columns of thread tx are the
+// float4s tx + 16 g of a row of D.  w has row pitch WP, n runs over N.
 template <int D, int RI, int N, int WP>
-__device__ __forceinline__ void cross_mix(const float* w, const float* m, int ty, int tx, float (&acc)[RI][D / 16]) {
+__device__ __forceinline__ void cross_mix(const float* w, const float* m, int ty, int tx, float2 (&acc)[RI][D / 32]) {
 #pragma unroll 2
   for (int n = 0; n < N; n += 4) {
     float4 x[RI];
@@ -97,28 +137,26 @@ __device__ __forceinline__ void cross_mix(const float* w, const float* m, int ty
 #pragma unroll
         for (int i = 0; i < RI; ++i) {
           const float p = e == 0 ? x[i].x : e == 1 ? x[i].y : e == 2 ? x[i].z : x[i].w;
-          acc[i][4 * g] = fmaf(p, y.x, acc[i][4 * g]);
-          acc[i][4 * g + 1] = fmaf(p, y.y, acc[i][4 * g + 1]);
-          acc[i][4 * g + 2] = fmaf(p, y.z, acc[i][4 * g + 2]);
-          acc[i][4 * g + 3] = fmaf(p, y.w, acc[i][4 * g + 3]);
+          acc[i][2 * g] = fma2(make_float2(p, p), make_float2(y.x, y.y), acc[i][2 * g]);
+          acc[i][2 * g + 1] = fma2(make_float2(p, p), make_float2(y.z, y.w), acc[i][2 * g + 1]);
         }
       }
   }
 }
 
-__device__ __forceinline__ void put4(float* p, float a, float b, float c, float d) {
-  *reinterpret_cast<float4*>(p) = make_float4(a, b, c, d);
-}
-__device__ __forceinline__ void put4(__nv_bfloat16* p, float a, float b, float c, float d) {
-  __nv_bfloat162 x[2] = {__floats2bfloat162_rn(a, b), __floats2bfloat162_rn(c, d)};
-  *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(x);
-}
-
-template <int D, typename T>
-__device__ __forceinline__ void cross_put(T* p, const float (&x)[D / 16], int tx, float f) {
+template <int D>
+__device__ __forceinline__ void cross_put(float* p, const float2 (&x)[D / 32], int tx, float f) {
 #pragma unroll
   for (int g = 0; g < D / 64; ++g)
-    put4(p + (tx + 16 * g) * 4, x[4 * g] * f, x[4 * g + 1] * f, x[4 * g + 2] * f, x[4 * g + 3] * f);
+    put4(p + (tx + 16 * g) * 4, x[2 * g].x * f, x[2 * g].y * f, x[2 * g + 1].x * f, x[2 * g + 1].y * f);
+}
+
+template <int RI, int N>
+__device__ __forceinline__ void cross_zero(float2 (&x)[RI][N]) {
+#pragma unroll
+  for (int i = 0; i < RI; ++i)
+#pragma unroll
+    for (int e = 0; e < N; ++e) x[i][e] = make_float2(0.f, 0.f);
 }
 
 __device__ __forceinline__ float half_warp_max(float x) {
@@ -132,59 +170,95 @@ __device__ __forceinline__ float half_warp_sum(float x) {
   return x;
 }
 
-// Forward: a CTA owns BM query rows of one head; 16 threads (a half warp)
-// share a row.  One pass over the keys in tiles of 64 with the running maximum
-// and sum; tiles without an allowed key are skipped.
-template <int D, int BM>
+// The key tiles of share z of n: [first, last) of the tiles of BN keys below len.
+__device__ __forceinline__ void cross_share(int len, int bn, int z, int n, int* first, int* last) {
+  const int64_t tiles = (len + bn - 1) / bn;
+  *first = (int)(tiles * z / n);
+  *last = (int)(tiles * (z + 1) / n);
+}
+
+// The next tile from t on that holds an allowed key, or `last`; the threads of
+// the block agree on it.  (With key lengths alone every tile below the length.)
+template <int BN>
+__device__ __forceinline__ int cross_next(const CrossArgs& a, int b, int len, int t, int last) {
+  if (a.key_mask == nullptr) return t;
+  for (; t < last; ++t)
+    if (__syncthreads_or((int)threadIdx.x < BN && cross_allowed(a, b, len, t * BN + (int)threadIdx.x))) break;
+  return t;
+}
+
+// Forward: a CTA owns BM = 16 RI query rows of one head and share blockIdx.z
+// of its keys; 16 threads (a half warp) share a row.  One pass over the keys in
+// tiles of BN with the running maximum and sum.  The next keys load while the
+// values are used and the next values while the scores are formed.  splits > 1:
+// part [splits][batch * heads][Lq][D] and part_lse, joined by cross_join_kernel.
+template <int D, int RI>
 struct CrossFwdSimt {
-  static constexpr int BN = 64, RI = BM / 16;
-  static constexpr size_t bytes() { return ((BM + BN) * (D + 4) + BM * (BN + 4)) * sizeof(float); }
+  static constexpr int BM = 16 * RI, BN = 64;
+  static constexpr size_t bytes() { return ((BM + 2 * BN) * (D + 4) + BM * (BN + 4)) * sizeof(float); }
 };
 
-template <typename T, int D, int BM>
+template <int D, int RI>
 __global__ void __launch_bounds__(kCrossThreads) cross_fwd_simt_kernel(const CrossArgs a) {
-  constexpr int BN = 64, RI = BM / 16, NJ = BN / 16, PP = BN + 4;
+  using L = CrossFwdSimt<D, RI>;
+  constexpr int BM = L::BM, BN = L::BN, NJ = BN / 16, PP = BN + 4;
   extern __shared__ __align__(16) float cross_smem[];
   float* sq = cross_smem;
-  float* skv = sq + BM * (D + 4);  // the key tile, then the value tile
-  float* sp = skv + BN * (D + 4);
+  float* sk = sq + BM * (D + 4);
+  float* sv = sk + BN * (D + 4);
+  float* sp = sv + BN * (D + 4);
   const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
   const int b = blockIdx.y / a.heads, h = blockIdx.y % a.heads, hk = h / (a.heads / a.kv_heads);
   const int row0 = blockIdx.x * BM;
-  const T* q = static_cast<const T*>(a.q) + b * a.sq.b + h * a.sq.h + (int64_t)row0 * a.sq.r;
-  const T* k = static_cast<const T*>(a.k) + b * a.sk.b + hk * a.sk.h;
-  const T* v = static_cast<const T*>(a.v) + b * a.sv.b + hk * a.sv.h;
+  const float* q = static_cast<const float*>(a.q) + b * a.sq.b + h * a.sq.h + (int64_t)row0 * a.sq.r;
+  const float* k = static_cast<const float*>(a.k) + b * a.sk.b + hk * a.sk.h;
+  const float* v = static_cast<const float*>(a.v) + b * a.sv.b + hk * a.sv.h;
   const int len = cross_len(a, b);
-  cross_tile<T, D, BM>(sq, q, a.sq.r, [&](int r) { return row0 + r < a.Lq; });
-  float m[RI], l[RI], o[RI][D / 16];
+  int t, last;
+  cross_share(len, BN, blockIdx.z, a.splits, &t, &last);
+  auto load_k = [&](int u) {
+    if (u < last)
+      cross_tile<D, BN>(sk, k + (int64_t)u * BN * a.sk.r, a.sk.r, [&](int r) { return cross_allowed(a, b, len, u * BN + r); });
+    cp_async_commit();
+  };
+  auto load_v = [&](int u) {
+    if (u < last)
+      cross_tile<D, BN>(sv, v + (int64_t)u * BN * a.sv.r, a.sv.r, [&](int r) { return cross_allowed(a, b, len, u * BN + r); });
+    cp_async_commit();
+  };
+  t = cross_next<BN>(a, b, len, t, last);
+  cross_tile<D, BM>(sq, q, a.sq.r, [&](int r) { return row0 + r < a.Lq; });
+  load_k(t);  // one group with the queries
+  load_v(t);
+  float m[RI], l[RI];
+  float2 o[RI][D / 32];
+  cross_zero(o);
 #pragma unroll
   for (int i = 0; i < RI; ++i) {
     m[i] = -INFINITY;
     l[i] = 0.f;
-#pragma unroll
-    for (int e = 0; e < D / 16; ++e) o[i][e] = 0.f;
   }
-  for (int n0 = 0; n0 < len; n0 += BN) {
-    auto ok = [&](int r) { return cross_allowed(a, b, len, n0 + r); };
-    if (!__syncthreads_or(threadIdx.x < BN && ok(threadIdx.x))) continue;  // also: the last tile's readers are done
-    cross_tile<T, D, BN>(skv, k + (int64_t)n0 * a.sk.r, a.sk.r, ok);
-    __syncthreads();
-    float x[RI][NJ] = {};
-    cross_dots<D, RI, NJ>(sq, skv, ty, tx, x);
+  while (t < last) {
+    const int next = cross_next<BN>(a, b, len, t + 1, last);
     bool on[NJ];
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) on[j] = ok(tx + 16 * j);
+    for (int j = 0; j < NJ; ++j) on[j] = cross_allowed(a, b, len, t * BN + tx + 16 * j);
+    cp_async_wait<1>();
+    __syncthreads();
+    float x[RI][NJ];
+    cross_dots<D, RI, NJ>(sq, sk, ty, tx, x);
+    __syncthreads();
+    load_k(next);
 #pragma unroll
     for (int i = 0; i < RI; ++i) {
-      float t = -INFINITY;
+      float top = m[i];
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
         x[i][j] = on[j] ? x[i][j] * a.scale : -INFINITY;
-        t = fmaxf(t, x[i][j]);
+        top = fmaxf(top, x[i][j]);
       }
-      const float top = fmaxf(m[i], half_warp_max(t));
-      const float base = top == -INFINITY ? 0.f : top;
-      const float f = expf(m[i] - base);
+      top = half_warp_max(top);
+      const float base = top == -INFINITY ? 0.f : top, f = expf(m[i] - base);
       m[i] = top;
       float sum = 0.f;
 #pragma unroll
@@ -195,37 +269,46 @@ __global__ void __launch_bounds__(kCrossThreads) cross_fwd_simt_kernel(const Cro
       }
       l[i] = l[i] * f + half_warp_sum(sum);
 #pragma unroll
-      for (int e = 0; e < D / 16; ++e) o[i][e] *= f;
+      for (int e = 0; e < D / 32; ++e) o[i][e] = make_float2(o[i][e].x * f, o[i][e].y * f);
     }
+    cp_async_wait<1>();
     __syncthreads();
-    cross_tile<T, D, BN>(skv, v + (int64_t)n0 * a.sv.r, a.sv.r, ok);
+    cross_mix<D, RI, BN, PP>(sp, sv, ty, tx, o);
     __syncthreads();
-    cross_mix<D, RI, BN, PP>(sp, skv, ty, tx, o);
+    load_v(next);
+    t = next;
   }
-  T* out = static_cast<T*>(a.out) + b * a.so.b + h * a.so.h;
+  cp_async_wait<0>();
+  const int64_t rows = (int64_t)a.batch * a.heads * a.Lq;
 #pragma unroll
   for (int i = 0; i < RI; ++i) {
     const int row = row0 + ty * RI + i;
     if (row >= a.Lq) continue;
-    cross_put<D>(out + (int64_t)row * a.so.r, o[i], tx, l[i] == 0.f ? 0.f : 1.f / l[i]);
-    if (a.lse != nullptr && tx == 0) a.lse[(int64_t)blockIdx.y * a.Lq + row] = m[i] + logf(l[i]);
+    const int64_t flat = (int64_t)blockIdx.y * a.Lq + row;
+    const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
+    if (a.splits > 1) {
+      cross_put<D>(a.part + (blockIdx.z * rows + flat) * D, o[i], tx, inv);
+      if (tx == 0) a.part_lse[blockIdx.z * rows + flat] = (m[i] + logf(l[i])) * kLog2e;
+    } else {
+      cross_put<D>(static_cast<float*>(a.out) + b * a.so.b + h * a.so.h + (int64_t)row * a.so.r, o[i], tx, inv);
+      if (a.lse != nullptr && tx == 0) a.lse[flat] = m[i] + logf(l[i]);
+    }
   }
 }
 
-// Backward, queries: a CTA owns 64 query rows; one pass over the keys in tiles
-// of 32.  Writes dq and delta.
-template <int D>
-struct CrossBwdSimt {
-  static constexpr int BM = 64, BN = 32;
-  static constexpr size_t dq_bytes() { return ((2 * BM + 2 * BN) * (D + 4) + BM * (BN + 4)) * sizeof(float); }
-  static constexpr size_t dkv_bytes() {
-    return ((2 * BM + 2 * BN) * (D + 4) + 2 * BM * (BN + 4) + 2 * BN) * sizeof(float);
-  }
+// Backward, queries: a CTA owns BM query rows and share blockIdx.z of their
+// keys; one pass over the keys in tiles of BN.  Writes dq and delta; splits > 1:
+// part [splits][batch * heads][Lq][D], added in order by cross_dq_sum_kernel.
+template <int D, int RI>
+struct CrossDqSimt {
+  static constexpr int BM = 16 * RI, BN = D == 64 ? 64 : 32;
+  static constexpr size_t bytes() { return ((2 * BM + 2 * BN) * (D + 4) + BM * (BN + 4)) * sizeof(float); }
 };
 
-template <typename T, int D>
+template <int D, int RI>
 __global__ void __launch_bounds__(kCrossThreads) cross_dq_simt_kernel(const CrossArgs a) {
-  constexpr int BM = CrossBwdSimt<D>::BM, BN = CrossBwdSimt<D>::BN, RI = BM / 16, NJ = BN / 16, PP = BN + 4;
+  using L = CrossDqSimt<D, RI>;
+  constexpr int BM = L::BM, BN = L::BN, NJ = BN / 16, PP = BN + 4;
   extern __shared__ __align__(16) float cross_smem[];
   float* sq = cross_smem;
   float* sg = sq + BM * (D + 4);
@@ -235,74 +318,100 @@ __global__ void __launch_bounds__(kCrossThreads) cross_dq_simt_kernel(const Cros
   const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
   const int b = blockIdx.y / a.heads, h = blockIdx.y % a.heads, hk = h / (a.heads / a.kv_heads);
   const int row0 = blockIdx.x * BM;
-  const T* o = static_cast<const T*>(a.o) + b * a.so.b + h * a.so.h;
-  const T* k = static_cast<const T*>(a.k) + b * a.sk.b + hk * a.sk.h;
-  const T* v = static_cast<const T*>(a.v) + b * a.sv.b + hk * a.sv.h;
+  const float* o = static_cast<const float*>(a.o) + b * a.so.b + h * a.so.h;
+  const float* k = static_cast<const float*>(a.k) + b * a.sk.b + hk * a.sk.h;
+  const float* v = static_cast<const float*>(a.v) + b * a.sv.b + hk * a.sv.h;
   const int len = cross_len(a, b);
+  int t, last;
+  cross_share(len, BN, blockIdx.z, a.splits, &t, &last);
+  auto load = [&](float* to, const float* base, int64_t pitch, int u) {
+    if (u < last)
+      cross_tile<D, BN>(to, base + (int64_t)u * BN * pitch, pitch, [&](int r) { return cross_allowed(a, b, len, u * BN + r); });
+    cp_async_commit();
+  };
+  t = cross_next<BN>(a, b, len, t, last);
   auto row_ok = [&](int r) { return row0 + r < a.Lq; };
-  cross_tile<T, D, BM>(sq, static_cast<const T*>(a.q) + b * a.sq.b + h * a.sq.h + (int64_t)row0 * a.sq.r,
-                           a.sq.r, row_ok);
-  cross_tile<T, D, BM>(sg, static_cast<const T*>(a.g) + b * a.sg.b + h * a.sg.h + (int64_t)row0 * a.sg.r,
-                           a.sg.r, row_ok);
+  cross_tile<D, BM>(sq, static_cast<const float*>(a.q) + b * a.sq.b + h * a.sq.h + (int64_t)row0 * a.sq.r, a.sq.r, row_ok);
+  cross_tile<D, BM>(sg, static_cast<const float*>(a.g) + b * a.sg.b + h * a.sg.h + (int64_t)row0 * a.sg.r, a.sg.r, row_ok);
+  cp_async_commit();
+  load(sk, k, a.sk.r, t);
+  load(sv, v, a.sv.r, t);
+  cp_async_wait<2>();
   __syncthreads();
-  float lse[RI], delta[RI], acc[RI][D / 16];
+  float lse[RI], delta[RI];
+  float2 acc[RI][D / 32];
+  cross_zero(acc);
 #pragma unroll
   for (int i = 0; i < RI; ++i) {
     const int row = row0 + ty * RI + i;
-    float t = 0.f;
+    float sum = 0.f;
     lse[i] = INFINITY;
     if (row < a.Lq) {
 #pragma unroll
       for (int c = tx * 4; c < D; c += 64) {
+        const float4 x = *reinterpret_cast<const float4*>(o + (int64_t)row * a.so.r + c);
         const float4 y = *reinterpret_cast<const float4*>(sg + (ty * RI + i) * (D + 4) + c);
-        const T* x = o + (int64_t)row * a.so.r + c;
-        t += to_float(x[0]) * y.x + to_float(x[1]) * y.y + to_float(x[2]) * y.z + to_float(x[3]) * y.w;
+        sum += x.x * y.x + x.y * y.y + x.z * y.z + x.w * y.w;
       }
       const float z = a.lse[(int64_t)blockIdx.y * a.Lq + row];
       lse[i] = z == -INFINITY ? INFINITY : z;  // no key: every p is zero
     }
-    delta[i] = half_warp_sum(t);
-    if (row < a.Lq && tx == 0) a.delta[(int64_t)blockIdx.y * a.Lq + row] = delta[i];
-#pragma unroll
-    for (int e = 0; e < D / 16; ++e) acc[i][e] = 0.f;
+    delta[i] = half_warp_sum(sum);
+    if (row < a.Lq && tx == 0 && blockIdx.z == 0) a.delta[(int64_t)blockIdx.y * a.Lq + row] = delta[i];
   }
-  for (int n0 = 0; n0 < len; n0 += BN) {
-    auto ok = [&](int r) { return cross_allowed(a, b, len, n0 + r); };
-    if (!__syncthreads_or(threadIdx.x < BN && ok(threadIdx.x))) continue;
-    cross_tile<T, D, BN>(sk, k + (int64_t)n0 * a.sk.r, a.sk.r, ok);
-    cross_tile<T, D, BN>(sv, v + (int64_t)n0 * a.sv.r, a.sv.r, ok);
+  while (t < last) {
+    const int next = cross_next<BN>(a, b, len, t + 1, last);
+    bool on[NJ];
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) on[j] = cross_allowed(a, b, len, t * BN + tx + 16 * j);
+    cp_async_wait<0>();
     __syncthreads();
-    float x[RI][NJ] = {}, dp[RI][NJ] = {};
-    cross_dots<D, RI, NJ>(sq, sk, ty, tx, x);
+    float x[RI][NJ], dp[RI][NJ];
     cross_dots<D, RI, NJ>(sg, sv, ty, tx, dp);
+    __syncthreads();
+    load(sv, v, a.sv.r, next);
+    cross_dots<D, RI, NJ>(sq, sk, ty, tx, x);
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-      const bool on = ok(tx + 16 * j);
+    for (int j = 0; j < NJ; ++j)
 #pragma unroll
-      for (int i = 0; i < RI; ++i) {
-        const float p = on ? expf(x[i][j] * a.scale - lse[i]) : 0.f;
-        ss[(ty * RI + i) * PP + tx + 16 * j] = on ? p * (dp[i][j] - delta[i]) : 0.f;
-      }
-    }
+      for (int i = 0; i < RI; ++i)
+        ss[(ty * RI + i) * PP + tx + 16 * j] = on[j] ? expf(x[i][j] * a.scale - lse[i]) * (dp[i][j] - delta[i]) : 0.f;
     __syncthreads();
     cross_mix<D, RI, BN, PP>(ss, sk, ty, tx, acc);
+    __syncthreads();
+    load(sk, k, a.sk.r, next);
+    t = next;
   }
-  T* dq = static_cast<T*>(a.dq) + b * a.sdq.b + h * a.sdq.h;
+  cp_async_wait<0>();
 #pragma unroll
   for (int i = 0; i < RI; ++i) {
     const int row = row0 + ty * RI + i;
-    if (row < a.Lq) cross_put<D>(dq + (int64_t)row * a.sdq.r, acc[i], tx, a.scale);
+    if (row >= a.Lq) continue;
+    const int64_t rows = (int64_t)a.batch * a.heads * a.Lq, flat = (int64_t)blockIdx.y * a.Lq + row;
+    if (a.splits > 1)
+      cross_put<D>(a.part + (blockIdx.z * rows + flat) * D, acc[i], tx, a.scale);
+    else
+      cross_put<D>(static_cast<float*>(a.dq) + b * a.sdq.b + h * a.sdq.h + (int64_t)row * a.sdq.r, acc[i], tx, a.scale);
   }
 }
 
 // Backward, keys: a CTA owns 64 keys of one key head and a contiguous share
 // (blockIdx.z of `splits`) of the query tiles of all heads that read it, in
-// order; its sums go to dk and dv, or with splits > 1 to partials that
-// cross_dkv_sum_kernel adds in split order (no atomics: results do not depend
-// on timing).
-template <typename T, int D>
+// order; its sums go to dk and dv, or with splits > 1 to part [splits][2][batch
+// * kv_heads][Lk][D], which cross_dkv_sum_kernel adds in split order (no
+// atomics: results do not depend on timing).
+template <int D>
+struct CrossDkvSimt {
+  static constexpr int BK = 64, BQ = D == 64 ? 64 : 32;
+  static constexpr size_t bytes() {
+    return ((2 * BK + 2 * BQ) * (D + 4) + 2 * BK * (BQ + 4) + 2 * BQ) * sizeof(float);
+  }
+};
+
+template <int D>
 __global__ void __launch_bounds__(kCrossThreads) cross_dkv_simt_kernel(const CrossArgs a) {
-  constexpr int BK = CrossBwdSimt<D>::BM, BQ = CrossBwdSimt<D>::BN, RI = BK / 16, NJ = BQ / 16, PP = BQ + 4;
+  using L = CrossDkvSimt<D>;
+  constexpr int BK = L::BK, BQ = L::BQ, RI = BK / 16, NJ = BQ / 16, PP = BQ + 4;
   extern __shared__ __align__(16) float cross_smem[];
   float* sk = cross_smem;
   float* sv = sk + BK * (D + 4);
@@ -317,15 +426,16 @@ __global__ void __launch_bounds__(kCrossThreads) cross_dkv_simt_kernel(const Cro
   const int n0 = blockIdx.x * BK;
   const int len = cross_len(a, b);
   auto ok = [&](int r) { return cross_allowed(a, b, len, n0 + r); };
-  float dk[RI][D / 16] = {}, dv[RI][D / 16] = {};
+  float2 dk[RI][D / 32], dv[RI][D / 32];
+  cross_zero(dk);
+  cross_zero(dv);
   bool on[RI];
 #pragma unroll
   for (int i = 0; i < RI; ++i) on[i] = ok(ty * RI + i);
-  if (__syncthreads_or(threadIdx.x < BK && ok(threadIdx.x))) {
-    cross_tile<T, D, BK>(sk, static_cast<const T*>(a.k) + b * a.sk.b + hk * a.sk.h + (int64_t)n0 * a.sk.r,
-                             a.sk.r, ok);
-    cross_tile<T, D, BK>(sv, static_cast<const T*>(a.v) + b * a.sv.b + hk * a.sv.h + (int64_t)n0 * a.sv.r,
-                             a.sv.r, ok);
+  if (__syncthreads_or((int)threadIdx.x < BK && ok(threadIdx.x))) {
+    cross_tile<D, BK>(sk, static_cast<const float*>(a.k) + b * a.sk.b + hk * a.sk.h + (int64_t)n0 * a.sk.r, a.sk.r, ok);
+    cross_tile<D, BK>(sv, static_cast<const float*>(a.v) + b * a.sv.b + hk * a.sv.h + (int64_t)n0 * a.sv.r, a.sv.r, ok);
+    cp_async_commit();
     const int per_head = (a.Lq + BQ - 1) / BQ;
     const int64_t tiles = (int64_t)per_head * group;
     const int64_t first = tiles * blockIdx.z / a.splits, last = tiles * (blockIdx.z + 1) / a.splits;
@@ -334,19 +444,22 @@ __global__ void __launch_bounds__(kCrossThreads) cross_dkv_simt_kernel(const Cro
       const int64_t bh = (int64_t)b * a.heads + h;
       auto row_ok = [&](int r) { return row0 + r < a.Lq; };
       __syncthreads();
-      cross_tile<T, D, BQ>(sq, static_cast<const T*>(a.q) + b * a.sq.b + h * a.sq.h + (int64_t)row0 * a.sq.r,
-                               a.sq.r, row_ok);
-      cross_tile<T, D, BQ>(sg, static_cast<const T*>(a.g) + b * a.sg.b + h * a.sg.h + (int64_t)row0 * a.sg.r,
-                               a.sg.r, row_ok);
+      cross_tile<D, BQ>(sq, static_cast<const float*>(a.q) + b * a.sq.b + h * a.sq.h + (int64_t)row0 * a.sq.r, a.sq.r, row_ok);
+      cp_async_commit();
+      cross_tile<D, BQ>(sg, static_cast<const float*>(a.g) + b * a.sg.b + h * a.sg.h + (int64_t)row0 * a.sg.r, a.sg.r, row_ok);
+      cp_async_commit();
       if (threadIdx.x < BQ) {
         const bool in = row_ok(threadIdx.x);
         const float z = in ? a.lse[bh * a.Lq + row0 + threadIdx.x] : -INFINITY;
         slse[threadIdx.x] = z == -INFINITY ? INFINITY : z;
         sdel[threadIdx.x] = in ? a.delta[bh * a.Lq + row0 + threadIdx.x] : 0.f;
       }
+      cp_async_wait<1>();
       __syncthreads();
-      float x[RI][NJ] = {}, dp[RI][NJ] = {};
+      float x[RI][NJ], dp[RI][NJ];
       cross_dots<D, RI, NJ>(sk, sq, ty, tx, x);
+      cp_async_wait<0>();
+      __syncthreads();
       cross_dots<D, RI, NJ>(sv, sg, ty, tx, dp);
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
@@ -362,14 +475,15 @@ __global__ void __launch_bounds__(kCrossThreads) cross_dkv_simt_kernel(const Cro
       cross_mix<D, RI, BQ, PP>(sp, sg, ty, tx, dv);
       cross_mix<D, RI, BQ, PP>(ss, sq, ty, tx, dk);
     }
+    cp_async_wait<0>();
   }
 #pragma unroll
   for (int i = 0; i < RI; ++i) {
     const int j = n0 + ty * RI + i;
     if (j >= a.Lk) continue;
     if (a.splits == 1) {
-      cross_put<D>(static_cast<T*>(a.dk) + b * a.sdk.b + hk * a.sdk.h + (int64_t)j * a.sdk.r, dk[i], tx, a.scale);
-      cross_put<D>(static_cast<T*>(a.dv) + b * a.sdv.b + hk * a.sdv.h + (int64_t)j * a.sdv.r, dv[i], tx, 1.f);
+      cross_put<D>(static_cast<float*>(a.dk) + b * a.sdk.b + hk * a.sdk.h + (int64_t)j * a.sdk.r, dk[i], tx, a.scale);
+      cross_put<D>(static_cast<float*>(a.dv) + b * a.sdv.b + hk * a.sdv.h + (int64_t)j * a.sdv.r, dv[i], tx, 1.f);
     } else {
       const int64_t rows = (int64_t)a.batch * a.kv_heads * a.Lk;
       float* p = a.part + ((int64_t)blockIdx.z * 2 * rows + (int64_t)blockIdx.y * a.Lk + j) * D;
@@ -379,27 +493,75 @@ __global__ void __launch_bounds__(kCrossThreads) cross_dkv_simt_kernel(const Cro
   }
 }
 
-// dk and dv from the partials, added in split order.  blockIdx.y: 0 dk, 1 dv.
-template <typename T, int D>
-__global__ void cross_dkv_sum_kernel(const CrossArgs a) {
-  const int64_t rows = (int64_t)a.batch * a.kv_heads * a.Lk;
-  const int64_t e = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * 4;
-  if (e >= rows * D) return;
+// Partials added in split order: out row (b, h, i) = sum_s part[s][row].
+struct CrossSumArgs {
+  const float* part;
+  int64_t rows, pitch;  // rows of one tensor, floats between two splits
+  float* out[2];
+  HeadView so[2];
+  int heads, L, splits;
+};
+
+// Grid y: the tensors that lie next to each other in a split (dk and dv), or one.
+template <int D>
+__global__ void __launch_bounds__(256) cross_sum_kernel(const CrossSumArgs a) {
+  const int64_t e = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (e >= a.rows * D) return;
   const int64_t row = e / D;
-  const int c = (int)(e % D), j = (int)(row % a.Lk);
-  const int bh = (int)(row / a.Lk), b = bh / a.kv_heads, hk = bh % a.kv_heads;
-  const float* p = a.part + blockIdx.y * rows * D + e;
+  const int c = (int)(e % D), i = (int)(row % a.L), bh = (int)(row / a.L), b = bh / a.heads, h = bh % a.heads;
+  const float* p = a.part + blockIdx.y * a.rows * D + e;
   float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
   for (int s = 0; s < a.splits; ++s) {
-    const float4 y = *reinterpret_cast<const float4*>(p + (int64_t)s * 2 * rows * D);
+    const float4 y = *reinterpret_cast<const float4*>(p + s * a.pitch);
     x.x += y.x;
     x.y += y.y;
     x.z += y.z;
     x.w += y.w;
   }
-  const HeadView& st = blockIdx.y == 0 ? a.sdk : a.sdv;
-  T* dst = static_cast<T*>(blockIdx.y == 0 ? a.dk : a.dv) + b * st.b + hk * st.h + (int64_t)j * st.r + c;
-  put4(dst, x.x, x.y, x.z, x.w);
+  const HeadView& st = a.so[blockIdx.y];
+  put4(a.out[blockIdx.y] + b * st.b + h * st.h + (int64_t)i * st.r + c, x.x, x.y, x.z, x.w);
+}
+
+// Joins the shares of a forward pass: out = sum_s w_s o_s / sum_s w_s with
+// w_s = 2^(lse_s - max).  D / 4 threads per row.
+struct CrossJoinArgs {
+  const float *part, *part_lse;  // [splits][rows][D], [splits][rows]
+  void* out;
+  HeadView so;
+  float* lse;  // or null
+  int64_t rows;
+  int heads, Lq, splits;
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(256) cross_join_kernel(const CrossJoinArgs a) {
+  const int64_t flat = (int64_t)blockIdx.x * (256 / (D / 4)) + threadIdx.x / (D / 4);
+  if (flat >= a.rows) return;
+  const int c = threadIdx.x % (D / 4) * 4;
+  float top = -INFINITY;
+#pragma unroll 4
+  for (int s = 0; s < a.splits; ++s) top = fmaxf(top, a.part_lse[s * a.rows + flat]);
+  float sum = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int s = 0; s < a.splits; ++s) {
+    const float z = a.part_lse[s * a.rows + flat];
+    if (z == -INFINITY) continue;  // a share without keys: its output was not written
+    const float w = exp2f(z - top);
+    const float4 y = *reinterpret_cast<const float4*>(a.part + (s * a.rows + flat) * D + c);
+    sum += w;
+    o.x += w * y.x;
+    o.y += w * y.y;
+    o.z += w * y.z;
+    o.w += w * y.w;
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const int bh = (int)(flat / a.Lq), b = bh / a.heads, h = bh % a.heads;
+  put4(static_cast<T*>(a.out) + b * a.so.b + h * a.so.h + (flat % a.Lq) * a.so.r + c, o.x * inv, o.y * inv, o.z * inv,
+       o.w * inv);
+  if (a.lse != nullptr && c == 0)
+    a.lse[flat] = top == -INFINITY ? top : (top + log2f(sum)) * 0.6931471805599453f;
 }
 
 }  // namespace pisa

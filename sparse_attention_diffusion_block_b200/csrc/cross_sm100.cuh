@@ -108,8 +108,6 @@ __global__ void __launch_bounds__(kPackThreads) cross_pack_kernel(const CrossPac
 //
 // TMEM columns: [0,128) S_A, [128,256) S_B, [256,256+D) O_A, [256+D,256+2D) O_B.
 struct CrossFwdArgs {
-  __nv_bfloat16* out;    // splits > 1: for the join
-  HeadView so;
   float* lse;            // [batch * heads][Lq] or null
   const int32_t* count;  // allowed keys per batch entry, or null: Lk
   float* part;           // splits > 1: [splits][batch * heads][Lq][D] outputs of each share
@@ -569,36 +567,6 @@ cross_fwd_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
   __syncthreads();
   fence_after_sync();
   if (warp == 9) tmem_dealloc(tmem, 512);
-}
-
-// Joins the shares: out = sum_s w_s o_s / sum_s w_s with w_s = 2^(lse_s - max).
-// D / 4 threads per row.
-template <int D>
-__global__ void __launch_bounds__(256) cross_join_kernel(const CrossFwdArgs a) {
-  const int64_t rows = (int64_t)a.BH * a.Lq;
-  const int64_t flat = (int64_t)blockIdx.x * (256 / (D / 4)) + threadIdx.x / (D / 4);
-  if (flat >= rows) return;
-  const int c = threadIdx.x % (D / 4) * 4;
-  float top = -INFINITY;
-  for (int s = 0; s < a.splits; ++s) top = fmaxf(top, a.part_lse[s * rows + flat]);
-  float sum = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s = 0; s < a.splits; ++s) {
-    const float z = a.part_lse[s * rows + flat];
-    if (z == -INFINITY) continue;
-    const float w = exp2f(z - top);
-    const float4 y = *reinterpret_cast<const float4*>(a.part + (s * rows + flat) * D + c);
-    sum += w;
-    o.x += w * y.x;
-    o.y += w * y.y;
-    o.z += w * y.z;
-    o.w += w * y.w;
-  }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  const int bh = (int)(flat / a.Lq), b = bh / a.heads, h = bh % a.heads;
-  put4(a.out + b * a.so.b + h * a.so.h + (flat % a.Lq) * a.so.r + c, o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-  if (a.lse != nullptr && c == 0)
-    a.lse[flat] = top == -INFINITY ? top : (top + log2f(sum)) * 0.6931471805599453f;
 }
 
 }  // namespace pisa

@@ -525,8 +525,7 @@ pisa_status run_cross_bwd_sm100(const CrossArgs& a, const CrossShape& s, char* w
   int sms = 0;
   if (!sm_count(&sms)) return PISA_ERR_CUDA;
   const size_t s1 = CrossDqLayout<D>::bytes(), s2 = CrossDkvLayout<D>::bytes();
-  static const bool regs = launch_registers(cross_dq_sm100_kernel<D>, kCrossRegs512) &&
-                           launch_registers(cross_dkv_sm100_kernel<D>, kDkvRegs);
+  static const bool regs = launch_registers(cross_dq_sm100_kernel<D>, kCrossRegs512);
   if (!regs || !set_smem(cross_dq_sm100_kernel<D>, s1) || !set_smem(cross_dkv_sm100_kernel<D>, s2))
     return PISA_ERR_CUDA;
   cross_dq_sm100_kernel<D><<<f.w.n_items < sms ? f.w.n_items : sms, kCrossThreads512, s1, st>>>(q128, g128, k64, v64, f);

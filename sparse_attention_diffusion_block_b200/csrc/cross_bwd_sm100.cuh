@@ -81,7 +81,9 @@ __global__ void __launch_bounds__(256) cross_delta_kernel(const CrossDeltaArgs a
 // Warps 0-3 / 4-7: rows of tile A / B, 8: TMA producer, 9: MMA issuer, 12-15:
 // epilogue (as in the forward kernel).  A key step's K stays until both tiles'
 // dQ have used it and its V only until both dP have, so K has three slots and V
-// two.  The queries and gradients of an item fill 128 KB and cannot be loaded
+// two; the end of the step in between frees one of each, so that one barrier
+// fills a step and one empties it (each commit and each wait costs the issuer
+// 80 to 190 cycles of a step's 3000).  The queries and gradients of an item fill 128 KB and cannot be loaded
 // ahead; they are brought into L2 one item early.
 //
 // delta_i = g_i . o_i comes from cross_delta_kernel, except with a single step
@@ -106,7 +108,7 @@ struct CrossDqLayout {
   static constexpr uint32_t kRows = 128u * D * 2u;  // one of Q, G of a tile
   static constexpr uint32_t kSlot = 64u * D * 2u;   // one of K, V of a step
   static constexpr uint32_t kStage = 4 * 4096;      // output rows of the four epilogue warps
-  static constexpr int kNumBars = 2 * (kDqK + kDqV) + 13;
+  static constexpr int kNumBars = 2 * kDqK + 13;
   static constexpr size_t bytes() {
     return 1024 + 4 * kRows + (kDqK + kDqV) * kSlot + kStage + kNumBars * 8 + 16;
   }
@@ -128,23 +130,21 @@ cross_dq_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
   uint8_t* sK = smem + 4 * ROWS;
   uint8_t* sV = sK + NK * SLOT;
   uint8_t* sStage = sV + NV * SLOT;
-  uint64_t* k_full = reinterpret_cast<uint64_t*>(sStage + Lay::kStage);
-  uint64_t* k_empty = k_full + NK;
-  uint64_t* v_full = k_empty + NK;
-  uint64_t* v_empty = v_full + NV;
-  uint64_t* q_full = v_empty + NV;   // [2]
+  uint64_t* full = reinterpret_cast<uint64_t*>(sStage + Lay::kStage);
+  uint64_t* freed = full + NK;       // event e: step e has been scored and step e - 1 is finished
+  uint64_t* q_full = freed + NK;     // [2]
   uint64_t* q_empty = q_full + 2;    // [2]
   uint64_t* s_full = q_empty + 2;    // [2]
   uint64_t* p_full = s_full + 2;     // [2]
   uint64_t* o_full = p_full + 2;     // [2]
   uint64_t* o_empty = o_full + 2;    // [2]
   uint64_t* mma_idle = o_empty + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(k_full + Lay::kNumBars);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(full + Lay::kNumBars);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < 2 * NK + 2 * NV; ++s) mbar_init(&k_full[s], 1);  // k_full .. v_empty
+    for (int s = 0; s < 2 * NK; ++s) mbar_init(&full[s], 1);  // full and freed
     for (int x = 0; x < 2; ++x) {
       mbar_init(&q_full[x], 1);
       mbar_init(&q_empty[x], 1);
@@ -185,19 +185,14 @@ cross_dq_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
       auto load = [&](const CrossItem& w, int u) {
         const int sk = it % NK, sv = it % NV;
         const int c2 = packed ? w.b * W.kv_heads + w.hk : w.hk, c3 = packed ? 0 : w.b;
-        if (!(ok = ok && mbar_wait(&k_empty[sk], ((it / NK) & 1) ^ 1, abort))) return;
-        mbar_expect_tx(&k_full[sk], SLOT);
+        // K of step it - 3 and V of step it - 2 are done with after event it - 2
+        if (it >= 2 && !(ok = ok && mbar_wait(&freed[(it - 2) % NK], ((it - 2) / NK) & 1, abort))) return;
+        mbar_expect_tx(&full[sk], 2 * SLOT);
 #pragma unroll
-        for (int cb = 0; cb < CB; ++cb)
-          tma_load_4d(sK + sk * SLOT + cb * 64 * 128, &tmK, &k_full[sk], cb * 64, u * 64, c2, c3);
-        if (!(ok = mbar_wait(&v_empty[sv], ((it / NV) & 1) ^ 1, abort))) {
-          mbar_drain(&k_full[sk], (it / NK) & 1);  // the one copy that the counts below do not cover
-          return;
+        for (int cb = 0; cb < CB; ++cb) {
+          tma_load_4d(sK + sk * SLOT + cb * 64 * 128, &tmK, &full[sk], cb * 64, u * 64, c2, c3);
+          tma_load_4d(sV + sv * SLOT + cb * 64 * 128, &tmV, &full[sk], cb * 64, u * 64, c2, c3);
         }
-        mbar_expect_tx(&v_full[sv], SLOT);
-#pragma unroll
-        for (int cb = 0; cb < CB; ++cb)
-          tma_load_4d(sV + sv * SLOT + cb * 64 * 128, &tmV, &v_full[sv], cb * 64, u * 64, c2, c3);
         ++it;
       };
       auto load_rows = [&](const CrossItem& w, int x) {
@@ -235,8 +230,7 @@ cross_dq_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
         for (int u = 2; ok && u < key_steps(cur); ++u) load(cur, u);
         cur = nxt;
       }
-      for (int u = it > NK ? it - NK : 0; u < it; ++u) mbar_drain(&k_full[u % NK], (u / NK) & 1);
-      for (int u = it > NV ? it - NV : 0; u < it; ++u) mbar_drain(&v_full[u % NV], (u / NV) & 1);
+      for (int u = it > NK ? it - NK : 0; u < it; ++u) mbar_drain(&full[u % NK], (u / NK) & 1);
       for (int x = 0; x < 2; ++x)
         if (nq[x] > 0) mbar_drain(&q_full[x], (nq[x] - 1) & 1);
     }
@@ -246,13 +240,12 @@ cross_dq_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
     constexpr uint32_t idS = idesc_bf16(128, 64, false, false);
     constexpr uint32_t idO = idesc_bf16(128, D, false, true);
     const uint32_t kring = smem_u32(sK), vring = smem_u32(sV), rows = smem_u32(sRows);
-    int it = 0, steps[2] = {0, 0}, nq[2] = {0, 0}, outs[2] = {0, 0};
+    int it = 0, events = 0, steps[2] = {0, 0}, nq[2] = {0, 0}, outs[2] = {0, 0};
     bool ok = true;
     auto take = [&](int& k, int& v) {
       k = it % NK;
       v = it % NV;
-      if (!(ok = ok && mbar_wait(&k_full[k], (it / NK) & 1, abort))) return;
-      if (!(ok = mbar_wait(&v_full[v], (it / NV) & 1, abort))) return;
+      if (!(ok = ok && mbar_wait(&full[k], (it / NK) & 1, abort))) return;
       fence_after_sync();
       ++it;
     };
@@ -284,7 +277,8 @@ cross_dq_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
     if (has) {
       take(ks, vs);
       for (int x = 0; ok && x < cur.tiles; ++x) s_mmas(x, ks, vs, true, key_steps(cur) == 1);
-      if (ok) mma_commit_warp(&v_empty[vs]);
+      if (ok) mma_commit_warp(&freed[0]);
+      events = 1;
     }
     while (ok && has) {
       i += gridDim.x;
@@ -315,8 +309,10 @@ cross_dq_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
           }
         }
         if (!ok) break;
-        mma_commit_warp(&k_empty[k0]);
-        if (next) mma_commit_warp(&v_empty[vs]);
+        if (next) {
+          mma_commit_warp(&freed[events % NK]);
+          ++events;
+        }
       }
       cur = nxt;
       has = more;
@@ -442,8 +438,11 @@ cross_dq_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
 // A CTA holds 128 keys and values and streams steps of 64 query rows:
 //   S^T = K Q^T, dP^T = V G^T (keys are TMEM lanes);  P^T and dS^T -> bf16 in
 //   place;  dV += P^T G,  dK += dS^T Q.
-// Even steps belong to warps 0-3, odd ones to warps 4-7, each with its own 128
-// columns of S^T and dP^T, so one's exponentials run under the other's MMAs.
+// Even steps belong to warps 0-7, odd ones to warps 8-15, each with its own 128
+// columns of S^T and dP^T, so one's exponentials run under the other's MMAs; two
+// threads share a key row, 32 query columns each, which halves the time between
+// a step's scores and its P (with one thread a row: 1500 of 3400 cycles per two
+// steps, 0.61 ms for 32760 x 512, 40 heads).  Warp 16 loads, warp 17 issues.
 // TMEM columns: [128x, +64) S^T, [128x + 64, +64) dP^T, [256, +D) dV, [256 + D, +D) dK.
 //
 // Work: the (batch, key head, key tile) items times the steps of all query
@@ -466,7 +465,7 @@ struct CrossDkvArgs {
   float scale_log2;
 };
 
-constexpr int kDkvStages = 4, kDkvThreads = 384, kDkvRegs = 168;
+constexpr int kDkvStages = 4, kDkvThreads = 640;
 
 template <int D>
 struct CrossDkvLayout {
@@ -475,7 +474,7 @@ struct CrossDkvLayout {
   static constexpr uint32_t kSlot = 2 * kHalf;
   static constexpr int kNumBars = 2 * kDkvStages + 2 + 2 + 2 + 2 + 1 + 1;  // even: what follows is 16-byte aligned
   static constexpr size_t bytes() {
-    return 1024 + 2 * kKeys + kDkvStages * kSlot + kNumBars * 8 + 16 + 8 * 2 * 128 * sizeof(float);
+    return 1024 + 2 * kKeys + kDkvStages * kSlot + kNumBars * 8 + 16 + 16 * 2 * 64 * sizeof(float);
   }
 };
 
@@ -574,7 +573,7 @@ cross_dkv_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
   uint64_t* mma_idle = epi_done + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(full + Lay::kNumBars);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  float* colv = reinterpret_cast<float*>(tmem_slot + 4);  // [8 warps][2 buffers][64 -lse2, 64 -delta]
+  float* colv = reinterpret_cast<float*>(tmem_slot + 4);  // [16 warps][2 buffers][32 -lse2, 32 -delta]
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (threadIdx.x == 0) {
@@ -586,15 +585,15 @@ cross_dkv_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
     mbar_init(kv_empty, 1);
     for (int x = 0; x < 2; ++x) {
       mbar_init(&s_full[x], 1);
-      mbar_init(&p_full[x], 128);
+      mbar_init(&p_full[x], 256);
     }
     mbar_init(o_full, 1);
-    mbar_init(epi_done, 256);
+    mbar_init(epi_done, 512);
     mbar_init(mma_idle, 1);
     *abort = 0;
     fence_mbar_init();
   }
-  if (warp == 9) {
+  if (warp == 17) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
@@ -605,10 +604,7 @@ cross_dkv_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
   const CrossKeySpace ks(a, gridDim.x);
   CrossPiece pc(ks);
 
-  // Registers: 2 x 128 x 200 + 128 x 104 = 384 x 168, the launch total.
-  if (warp >= 8) {
-   asm volatile("setmaxnreg.dec.sync.aligned.u32 104;\n" ::: "memory");
-   if (warp == 8) {
+  if (warp == 16) {
     // ================================================================ producer
     if (lane == 0) {
       prefetch_tensormap(&tmQ);
@@ -646,7 +642,7 @@ cross_dkv_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       if (nkv > 0) mbar_drain(kv_full, (nkv - 1) & 1);
     }
     __syncwarp();
-   } else if (warp == 9) {
+  } else if (warp == 17) {
     // ================================================================ MMA issuer
     constexpr uint32_t idS = idesc_bf16(128, 64, false, false);
     constexpr uint32_t idO = idesc_bf16(128, D, false, true);
@@ -689,11 +685,11 @@ cross_dkv_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
         const uint32_t qb = ring + s * SLOT;
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          mma_ts_warp(tmem + DV, tmem + x * 128 + kk * 8, desc_sw128(qb + HALF + kk * 16 * 128, 64 * 128, 1024), idO,
+          mma_ts_warp(tmem + DV, tmem + x * 128 + (kk >> 1) * 32 + (kk & 1) * 8, desc_sw128(qb + HALF + kk * 16 * 128, 64 * 128, 1024), idO,
                       (t > 0 || kk > 0) ? 1u : 0u);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          mma_ts_warp(tmem + DK, tmem + x * 128 + 64 + kk * 8, desc_sw128(qb + kk * 16 * 128, 64 * 128, 1024), idO,
+          mma_ts_warp(tmem + DK, tmem + x * 128 + 64 + (kk >> 1) * 32 + (kk & 1) * 8, desc_sw128(qb + kk * 16 * 128, 64 * 128, 1024), idO,
                       (t > 0 || kk > 0) ? 1u : 0u);
         mma_commit_warp(&empty[s]);
         if (t + 2 < pc.n) s_mmas(x);
@@ -707,42 +703,32 @@ cross_dkv_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
     mma_commit_warp(mma_idle);
     mbar_drain(mma_idle, 0);
     __syncwarp();
-   }
-  } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;\n" ::: "memory");
-    // ================================================================ keys as rows: even steps (warps 0-3), odd (4-7)
-    const int x = warp / 4, row = threadIdx.x % 128;
+  } else if (warp < 16) {
+    // ================================================================ keys as rows: even steps (warps 0-7), odd (8-15)
+    const int x = warp / 8, half = warp / 4 % 2, row = threadIdx.x % 128;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp % 4) * 32) << 16);
-    const uint32_t sbase = lane_base + x * 128;
+    const uint32_t sbase = lane_base + x * 128 + half * 32;  // this thread's scores; its P goes over their first half
     const uint64_t c2x2 = f2_pack(a.scale_log2, a.scale_log2);
-    // Each warp keeps its own copy of a step's 64 -lse2 and -delta (two rows a
+    // Each warp keeps its own copy of its 32 columns' -lse2 and -delta (a row a
     // lane, read one step ahead), so that no barrier but the bounded ones
     // stands between warps.  A row past the end gives p = 0.
-    float* cv = colv + warp * 256;
-    auto columns = [&](int u) -> float4 {
-      const int q = u % ks.per_head * 64 + 2 * lane;
+    float* cv = colv + warp * 128;
+    auto columns = [&](int u) -> float2 {
+      const int q = u % ks.per_head * 64 + half * 32 + lane;
+      if (q >= a.Lq) return make_float2(-INFINITY, 0.f);
       const int64_t at = ((int64_t)pc.b * a.heads + pc.hk * ks.group + u / ks.per_head) * a.Lq + q;
-      float4 v = make_float4(-INFINITY, -INFINITY, 0.f, 0.f);
-      if (q < a.Lq) {
-        v.x = -a.lse[at] * kLog2e;
-        v.z = -a.delta[at];
-      }
-      if (q + 1 < a.Lq) {
-        v.y = -a.lse[at + 1] * kLog2e;
-        v.w = -a.delta[at + 1];
-      }
-      return v;
+      return make_float2(-a.lse[at] * kLog2e, -a.delta[at]);
     };
     int gs = 0, mine = 0, pieces = 0;
     bool ok = true;
     while (ok && pc.next(ks, a)) {
       int t = (gs + x) & 1;  // this warpgroup's first step: gs + t has parity x
-      float4 cval = make_float4(0.f, 0.f, 0.f, 0.f);
+      float2 cval = make_float2(0.f, 0.f);
       if (t < pc.n) cval = columns(pc.u0 + t);
       for (; t < pc.n; t += 2, ++mine) {
-        float* cb = cv + (mine & 1) * 128;
-        *reinterpret_cast<float2*>(cb + 2 * lane) = make_float2(cval.x, cval.y);
-        *reinterpret_cast<float2*>(cb + 64 + 2 * lane) = make_float2(cval.z, cval.w);
+        float* cb = cv + (mine & 1) * 64;
+        cb[lane] = cval.x;
+        cb[32 + lane] = cval.y;
         __syncwarp();
         if (t + 2 < pc.n) cval = columns(pc.u0 + t + 2);
         if (!__all_sync(0xffffffffu, mbar_wait(&s_full[x], mine & 1, abort))) {
@@ -750,35 +736,30 @@ cross_dkv_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
           break;
         }
         fence_after_sync();
-        uint32_t s[64], dp[64];
+        uint32_t s[32], dp[32];
         tmem_ld32(sbase, s);
-        tmem_ld32(sbase + 32, s + 32);
         tmem_ld32(sbase + 64, dp);
-        tmem_ld32(sbase + 96, dp + 32);
         tmem_wait_ld();
+        uint32_t pk[16], dk[16];
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          uint32_t pk[16], dk[16];
+        for (int c = 0; c < 32; c += 4) {
+          const ulonglong2 nl = *reinterpret_cast<const ulonglong2*>(cb + c);
+          const ulonglong2 nd = *reinterpret_cast<const ulonglong2*>(cb + 32 + c);
 #pragma unroll
-          for (int c = 0; c < 32; c += 4) {
-            const ulonglong2 nl = *reinterpret_cast<const ulonglong2*>(cb + hh * 32 + c);
-            const ulonglong2 nd = *reinterpret_cast<const ulonglong2*>(cb + 64 + hh * 32 + c);
-#pragma unroll
-            for (int e = 0; e < 4; e += 2) {
-              const int i = hh * 32 + c + e;
-              const uint64_t y = ffma2(f2_pack(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), c2x2,
-                                       e == 0 ? nl.x : nl.y);
-              const float p0 = ex2(f2_lo(y)), p1 = ex2(f2_hi(y));
-              const uint64_t g = fadd2(f2_pack(__uint_as_float(dp[i]), __uint_as_float(dp[i + 1])),
-                                       e == 0 ? nd.x : nd.y);
-              const uint64_t z = fmul2(f2_pack(p0, p1), g);
-              pk[(c + e) >> 1] = pack_bf16x2(p0, p1);
-              dk[(c + e) >> 1] = pack_bf16x2(f2_lo(z), f2_hi(z));
-            }
+          for (int e = 0; e < 4; e += 2) {
+            const int i = c + e;
+            const uint64_t y = ffma2(f2_pack(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), c2x2,
+                                     e == 0 ? nl.x : nl.y);
+            const float p0 = ex2(f2_lo(y)), p1 = ex2(f2_hi(y));
+            const uint64_t g = fadd2(f2_pack(__uint_as_float(dp[i]), __uint_as_float(dp[i + 1])),
+                                     e == 0 ? nd.x : nd.y);
+            const uint64_t z = fmul2(f2_pack(p0, p1), g);
+            pk[i >> 1] = pack_bf16x2(p0, p1);
+            dk[i >> 1] = pack_bf16x2(f2_lo(z), f2_hi(z));
           }
-          tmem_st16(sbase + hh * 16, pk);
-          tmem_st16(sbase + 64 + hh * 16, dk);
         }
+        tmem_st16(sbase, pk);
+        tmem_st16(sbase + 64, dk);
         tmem_wait_st();
         fence_before_sync();
         mbar_arrive(&p_full[x]);
@@ -788,11 +769,11 @@ cross_dkv_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       if (!__all_sync(0xffffffffu, mbar_wait(o_full, pieces & 1, abort))) break;
       ++pieces;
       fence_after_sync();
-      // warps 0-3 write dv, 4-7 dk
+      // warps 0-7 write dv, 8-15 dk, half of the columns each
       float* dst = a.part + (pc.slot * 2 + x) * 128 * D + row * D;
       const bool in = pc.j * 128 + row < pc.nv;
 #pragma unroll 1
-      for (int ch = 0; ch < D / 32; ++ch) {
+      for (int ch = half * (D / 64); ch < (half + 1) * (D / 64); ++ch) {
         uint32_t o[32];
         tmem_ld32(lane_base + (x == 0 ? DV : DK) + ch * 32, o);
         tmem_wait_ld();
@@ -810,7 +791,7 @@ cross_dkv_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
-  if (warp == 9) tmem_dealloc(tmem, 512);
+  if (warp == 17) tmem_dealloc(tmem, 512);
 }
 
 // dv (blockIdx.y = 0) and dk (1): the pieces of each key row in CTA order, the

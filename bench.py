@@ -442,6 +442,70 @@ def run_ablation(args):
     return 0
 
 
+BLOCK_STATES = 512  # encoder states of the block's cross-attention
+
+
+def run_block(cfg, keep):
+    """The attention of one transformer block at a workload's shape, operator by
+    operator: rotary positions out of a fused projection, the piecewise sparse
+    self-attention, cross-attention to BLOCK_STATES encoder states, and the
+    gradients of the last and of the positions.  Seeded noise on the device;
+    times are medians of CUDA-event pairs, caches as the operator before left
+    them."""
+    import torch
+    import sparse_attention_diffusion_block_b200 as pisa
+    dev = torch.device("cuda", 0)
+    torch.cuda.set_device(dev)
+    gen = torch.Generator(device=dev).manual_seed(cfg.seed)
+    dt = torch.bfloat16 if cfg.dtype == "bf16" else torch.float32
+    b, h, L, d = cfg.batch, cfg.heads, cfg.L, cfg.d
+
+    def noise(*shape):
+        return torch.randn(*shape, device=dev, generator=gen).to(dt)
+
+    def heads_first(x):
+        return x.permute(0, 2, 1, 3)
+
+    grid = cfg.grid or (L,)
+    pos = torch.stack([x.flatten() for x in torch.meshgrid(
+        *(torch.arange(n, device=dev, dtype=torch.float32) for n in grid), indexing="ij")], 1).contiguous()
+    pairs = [d // 2 // len(grid)] * len(grid)
+    pairs[0] += d // 2 - sum(pairs)
+    dims = tuple(2 * p for p in pairs)  # (44, 42, 42) for three axes of 128
+    qkv = noise(b, L, 3, h, d)
+    q, k, v = (heads_first(qkv[:, :, i]) for i in range(3))
+    text = noise(b, BLOCK_STATES, 2, h, d)
+    tk, tv = (heads_first(text[:, :, i]) for i in range(2))
+    g = heads_first(noise(b, L, h, d))
+    vd = v.contiguous()
+    q1, k1 = pisa.rope(q, k, pos, dims)
+    x = pisa.attn_fwd(q1, k1, vd, cfg.block, cfg.keep_ratio)
+    out, lse = pisa.cross_attn_fwd(x, tk, tv, return_lse=True)
+    steps = {
+        "rope": lambda: pisa.rope(q, k, pos, dims, q_out=q1, k_out=k1),
+        "attn_fwd": lambda: pisa.attn_fwd(q1, k1, vd, cfg.block, cfg.keep_ratio, out=x),
+        "cross_attn_fwd": lambda: pisa.cross_attn_fwd(x, tk, tv, return_lse=True, out=out),
+        "cross_attn_bwd": lambda: pisa.cross_attn_bwd(g, x, tk, tv, out, lse),
+        "rope_bwd": lambda: pisa.rope_bwd(q1, k1, pos, dims, q_out=q, k_out=k),
+    }
+    ev = {n: [] for n in steps}
+    for i in range(13):
+        for n, f in steps.items():
+            a, z = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            f()
+            z.record()
+            ev[n].append((a, z))
+    torch.cuda.synchronize()
+    if pisa.device_status() != 0:
+        raise RuntimeError("device status set")
+    ms = {n: statistics.median(a.elapsed_time(z) for a, z in e[3:]) for n, e in ev.items()}
+    print(json.dumps({"block": "attention operators of one transformer block", "data": "synthetic",
+                      "dtype": cfg.dtype, "config": describe(cfg, keep) + f", {BLOCK_STATES} encoder states",
+                      "axis_dims": dims, "ms": ms}), flush=True)
+    return 0
+
+
 def max_over_ranks(x: float, dist, device) -> float:
     """The maximum of ``x`` over all ranks (the slowest rank's time); ``x``
     itself when not distributed."""
@@ -537,6 +601,9 @@ def main():
     ap.add_argument("--ablation", action="store_true",
                     help="first-order term ablation (hybrid vs per-block H_j) on small shapes instead of the "
                          "bench line")
+    ap.add_argument("--block", action="store_true",
+                    help="time the attention operators of one transformer block at the workload's shape "
+                         "(rotary positions, self-attention, cross-attention, gradients) instead of the bench line")
     ap.add_argument("--no-dense-reference", action="store_true",
                     help="skip the dense-attention context (every block selected; torch SDPA)")
     ap.add_argument("--e2e-chunk", type=int, default=2,
@@ -560,6 +627,9 @@ def main():
         return run_sweep(args)
     if args.ablation:
         return run_ablation(args)
+    if args.block:
+        import oracle
+        return run_block(cfg, oracle.keep_count(cfg.L, cfg.block, cfg.keep_ratio))
     if args.impl == "reference":
         import oracle  # reference arm: the oracle as it stands
         return run_reference(args, cfg, oracle.keep_count(cfg.L, cfg.block, cfg.keep_ratio))

@@ -212,28 +212,34 @@ struct CrossFwdPlan {
   size_t part, part_lse, total;
 };
 
-// Tensor-core forward: shares of a head's key tiles.  The time follows the
-// waves of CTAs (one per SM) times the steps of one, of which about two go to
-// its start and end; joining the shares costs a launch (about two steps) and
-// takes their outputs through memory in 32 bits (one step: about 8 MB), so it
-// pays where there are few rows and long keys: 80 heads of one tile of rows and
-// 36 of keys, 66 us without shares.
+// Tensor-core kernels over query tiles: shares of a head's key tiles.  The time
+// follows the waves of CTAs (one per SM) times the steps of one, of which about
+// two go to its start and end; joining the shares costs a launch (about two
+// steps) and takes their outputs through memory in 32 bits (one step: about 8
+// MB), so it pays where there are few rows and long keys: 80 heads of one tile
+// of rows and 36 of keys, forward, 66 us without shares and 54 with three.
+int cross_tile_splits(const CrossShape& s) {
+  const long long items = (long long)s.batch * s.heads * (((s.Lq + 127) / 128 + 1) / 2), tiles = (s.Lk + 127) / 128;
+  const double step_bytes = 8e6, out = 8.0 * s.batch * s.heads * s.Lq * s.d;  // written and read
+  int splits = 1;
+  double best = 0.0;
+  for (int n = 1; n <= tiles && n <= 32 && (n == 1 || items * n <= 4 * kSMs); ++n) {
+    const double waves = (double)((items * n + kSMs - 1) / kSMs);
+    const double cost = waves * ((tiles + n - 1) / n + 2) + (n > 1 ? 2.0 + n * out / step_bytes : 0.0);
+    if (n == 1 || cost < best) {
+      best = cost;
+      splits = n;
+    }
+  }
+  return splits;
+}
+
 CrossFwdPlan cross_fwd_plan(const CrossShape& s) {
   CrossFwdPlan p{};
   p.splits = 1;
   if (s.dtype == PISA_BF16 && !cross_few_rows(s)) {
     p.pack = cross_pack_plan(s, false);
-    const long long items = (long long)s.batch * s.heads * (((s.Lq + 127) / 128 + 1) / 2), tiles = (s.Lk + 127) / 128;
-    const double step_bytes = 8e6, out = 8.0 * s.batch * s.heads * s.Lq * s.d;  // written and read
-    double best = 0.0;
-    for (int n = 1; n <= tiles && n <= 32 && (n == 1 || items * n <= 4 * kSMs); ++n) {
-      const double waves = (double)((items * n + kSMs - 1) / kSMs);
-      const double cost = waves * ((tiles + n - 1) / n + 2) + (n > 1 ? 2.0 + n * out / step_bytes : 0.0);
-      if (n == 1 || cost < best) {
-        best = cost;
-        p.splits = n;
-      }
-    }
+    p.splits = cross_tile_splits(s);
   } else if (!cross_few_rows(s)) {
     p.splits = cross_simt_splits(s, 64);
   }
@@ -249,13 +255,13 @@ CrossFwdPlan cross_fwd_plan(const CrossShape& s) {
 struct CrossBwdPlan {
   CrossPackPlan pack;
   int splits;     // dk/dv: CUDA cores, shares of the query tiles; tensor cores, CTAs
-  int dq_splits;  // CUDA cores: shares of the keys
+  int dq_splits;  // shares of the keys in the dq kernel
   size_t delta, part, total;
 };
 
 // fp32: query shares per key tile, enough CTAs for two per SM, at least two
 // query tiles each, and partials of at most 256 MB.  bf16: one CTA per SM, but
-// at least eight steps of 64 query rows each.
+// at least eight steps of 64 query rows each, or one key tile's where it has fewer.
 CrossBwdPlan cross_bwd_plan(const CrossShape& s) {
   CrossBwdPlan p{};
   const long long group = s.heads / s.kv_heads, slices = (long long)s.batch * s.kv_heads;
@@ -265,9 +271,14 @@ CrossBwdPlan cross_bwd_plan(const CrossShape& s) {
     // with a mask any number of CTAs, otherwise equal ranges of every key tile's steps
     const long long tiles = (s.Lk + 127) / 128, items = slices * tiles, steps = slices * group * ((s.Lq + 63) / 64);
     const long long lanes = s.masked ? 1 : tiles, all = s.masked ? steps * tiles : steps;
-    const long long most = (all + 7) / 8, n = kSMs / lanes < 1 ? 1 : kSMs / lanes;
+    const long long item = group * ((s.Lq + 63) / 64), least = item < 8 ? item : 8;
+    const long long most = (all + least - 1) / least, n = kSMs / lanes < 1 ? 1 : kSMs / lanes;
     p.splits = (int)(lanes * (n < most ? n : most));
-    p.part = align_up((size_t)(items + p.splits) * 2 * 128 * s.d * sizeof(float));
+    p.dq_splits = cross_tile_splits(s);
+    // the two kernels' partials, one after the other in the same place
+    const size_t kv = (size_t)(items + p.splits) * 2 * 128 * s.d * sizeof(float);
+    const size_t dq = p.dq_splits > 1 ? (size_t)p.dq_splits * s.batch * s.heads * s.Lq * s.d * sizeof(float) : 0;
+    p.part = align_up(kv > dq ? kv : dq);
   } else {
     const int bq = s.d == 64 ? 64 : 32;
     const long long ctas = slices * ((s.Lk + 63) / 64), tiles = group * ((s.Lq + bq - 1) / bq);
@@ -496,6 +507,15 @@ struct CrossFwdOp {
   }
 };
 
+// dq from the sums of its shares.
+template <typename T, int D>
+pisa_status launch_cross_dq_sum(const CrossArgs& a, const CrossShape& s, int splits, const float* part, cudaStream_t st) {
+  const int64_t rows = (int64_t)s.batch * s.heads * s.Lq;
+  const CrossSumArgs c{part, rows, rows * D, {a.dq, nullptr}, {a.sdq, a.sdq}, s.heads, s.Lq, splits};
+  cross_sum_kernel<T, D><<<dim3((unsigned)((rows * (D / 4) + 255) / 256), 1), 256, 0, st>>>(c);
+  return last_launch();
+}
+
 template <int D>
 pisa_status run_cross_bwd_sm100(const CrossArgs& a, const CrossShape& s, char* ws, cudaStream_t st) {
   const CrossBwdPlan p = cross_bwd_plan(s);
@@ -513,7 +533,8 @@ pisa_status run_cross_bwd_sm100(const CrossArgs& a, const CrossShape& s, char* w
   f.sdq = a.sdq;
   f.lse = a.lse;
   f.delta = reinterpret_cast<float*>(ws + p.pack.total);
-  f.w = cross_work(s, x.count, 1);
+  f.w = cross_work(s, x.count, p.dq_splits);
+  f.w.part = reinterpret_cast<float*>(ws + p.pack.total + p.delta);
   f.scale = a.scale;
   if (s.Lk > 64) {  // up to 64 keys the dq kernel forms delta itself
     const CrossDeltaArgs d{static_cast<const __nv_bfloat16*>(a.g), static_cast<const __nv_bfloat16*>(a.o), a.sg, a.so,
@@ -530,6 +551,8 @@ pisa_status run_cross_bwd_sm100(const CrossArgs& a, const CrossShape& s, char* w
     return PISA_ERR_CUDA;
   cross_dq_sm100_kernel<D><<<f.w.n_items < sms ? f.w.n_items : sms, kCrossThreads512, s1, st>>>(q128, g128, k64, v64, f);
   if (last_launch() != PISA_OK) return PISA_ERR_CUDA;
+  if (p.dq_splits > 1)
+    if (pisa_status e = launch_cross_dq_sum<__nv_bfloat16, D>(a, s, p.dq_splits, f.w.part, st)) return e;
   CrossReduceArgs r{};
   r.a = CrossDkvArgs{a.lse, f.delta, x.count, reinterpret_cast<float*>(ws + p.pack.total + p.delta),
                      s.batch, s.heads, s.kv_heads, s.Lq, s.Lk, f.w.scale_log2};
@@ -542,9 +565,7 @@ pisa_status run_cross_bwd_sm100(const CrossArgs& a, const CrossShape& s, char* w
   r.ctas = p.splits;
   cross_dkv_sm100_kernel<D><<<p.splits, kDkvThreads, s2, st>>>(q64, g64, k128, v128, r.a);
   if (last_launch() != PISA_OK) return PISA_ERR_CUDA;
-  constexpr int rows = 256 / (D / 4);
-  const long long n = ((long long)s.batch * s.kv_heads * s.Lk + rows - 1) / rows;
-  cross_dkv_reduce_kernel<D><<<dim3((unsigned)n, 2), 256, 0, st>>>(r);
+  cross_dkv_reduce_kernel<D><<<dim3((s.Lk + kReduceKeys - 1) / kReduceKeys, s.batch * s.kv_heads, 2), 256, 0, st>>>(r);
   return last_launch();
 }
 
@@ -565,21 +586,17 @@ pisa_status run_cross_bwd_simt(CrossArgs a, const CrossShape& s, char* ws, cudaS
   a.splits = p.dq_splits;
   if (pisa_status e = cross_simt_ri(s) == 4 ? launch_cross_dq_simt<D, 4>(a, s, st) : launch_cross_dq_simt<D, 1>(a, s, st))
     return e;
-  if (p.dq_splits > 1) {
-    const int64_t rows = (int64_t)s.batch * s.heads * s.Lq;
-    CrossSumArgs c{a.part, rows, rows * D, {static_cast<float*>(a.dq), nullptr}, {a.sdq, a.sdq}, s.heads, s.Lq, p.dq_splits};
-    cross_sum_kernel<D><<<dim3((unsigned)((rows * (D / 4) + 255) / 256), 1), 256, 0, st>>>(c);
-    if (last_launch() != PISA_OK) return PISA_ERR_CUDA;
-  }
+  if (p.dq_splits > 1)
+    if (pisa_status e = launch_cross_dq_sum<float, D>(a, s, p.dq_splits, a.part, st)) return e;
   a.splits = p.splits;
   constexpr size_t smem = CrossDkvSimt<D>::bytes();
   if (!set_smem(cross_dkv_simt_kernel<D>, smem)) return PISA_ERR_CUDA;
   cross_dkv_simt_kernel<D><<<dim3((s.Lk + 63) / 64, s.batch * s.kv_heads, a.splits), kCrossThreads, smem, st>>>(a);
   if (last_launch() != PISA_OK || p.splits == 1) return last_launch();
   const int64_t rows = (int64_t)s.batch * s.kv_heads * s.Lk;
-  CrossSumArgs c{a.part, rows, 2 * rows * D, {static_cast<float*>(a.dk), static_cast<float*>(a.dv)}, {a.sdk, a.sdv},
+  CrossSumArgs c{a.part, rows, 2 * rows * D, {a.dk, a.dv}, {a.sdk, a.sdv},
                  s.kv_heads, s.Lk, p.splits};
-  cross_sum_kernel<D><<<dim3((unsigned)((rows * (D / 4) + 255) / 256), 2), 256, 0, st>>>(c);
+  cross_sum_kernel<float, D><<<dim3((unsigned)((rows * (D / 4) + 255) / 256), 2), 256, 0, st>>>(c);
   return last_launch();
 }
 

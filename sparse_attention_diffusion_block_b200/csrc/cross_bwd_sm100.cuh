@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(256) cross_delta_kernel(const CrossDeltaArgs a
 // 80 to 190 cycles of a step's 3000).  The queries and gradients of an item fill 128 KB and cannot be loaded
 // ahead; they are brought into L2 one item early.
 //
-// delta_i = g_i . o_i comes from cross_delta_kernel, except with a single step
+// delta_i = g_i . o_i comes from cross_delta_kernel, except with at most one step
 // of keys: there it is sum_j p_ij dp_ij, formed in 32 bits from what the row
 // holds (and written for the dk/dv kernel).  With few keys ds is a small
 // difference of dp and delta, and the rounding of the stored bf16 output would
@@ -97,7 +97,7 @@ struct CrossDqArgs {
   HeadView sdq;
   const float* lse;
   float* delta;
-  CrossFwdArgs w;  // shape of the work: heads, kv_heads, Lq, Lk, pairs, count (splits = 1)
+  CrossFwdArgs w;  // the shape of the work; part: [splits][batch * heads][Lq][D] sums of each share
   float scale;
 };
 
@@ -168,7 +168,7 @@ cross_dq_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
   const CrossFwdArgs& W = a.w;
   const int n_items = W.n_items;
   // An item's key steps of 64 (CrossItem counts tiles of 128).
-  auto key_steps = [](const CrossItem& w) { return (w.nv + 63) / 64; };
+  auto key_steps = [](const CrossItem& w) { return (min(w.nv - w.j0 * 128, w.T * 128) + 63) / 64; };
 
   if (warp >= 8 && warp < 12) {
    fewer_registers<96>();
@@ -190,8 +190,8 @@ cross_dq_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
         mbar_expect_tx(&full[sk], 2 * SLOT);
 #pragma unroll
         for (int cb = 0; cb < CB; ++cb) {
-          tma_load_4d(sK + sk * SLOT + cb * 64 * 128, &tmK, &full[sk], cb * 64, u * 64, c2, c3);
-          tma_load_4d(sV + sv * SLOT + cb * 64 * 128, &tmV, &full[sk], cb * 64, u * 64, c2, c3);
+          tma_load_4d(sK + sk * SLOT + cb * 64 * 128, &tmK, &full[sk], cb * 64, w.j0 * 128 + u * 64, c2, c3);
+          tma_load_4d(sV + sv * SLOT + cb * 64 * 128, &tmV, &full[sk], cb * 64, w.j0 * 128 + u * 64, c2, c3);
         }
         ++it;
       };
@@ -339,7 +339,7 @@ cross_dq_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
       const bool in = x < v.tiles && qrow < W.Lq;
       const int64_t flat = (int64_t)v.bh * W.Lq + qrow;
       nl = in ? -a.lse[flat] * kLog2e : -INFINITY;
-      nd = in && key_steps(v) > 1 ? -a.delta[flat] : 0.f;
+      nd = in && v.nv > 64 ? -a.delta[flat] : 0.f;
     };
     int i = blockIdx.x;
     bool has = w.with_keys(W, i);
@@ -370,12 +370,12 @@ cross_dq_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
           s[c] = __float_as_uint(ex2(f2_lo(t)));
           s[c + 1] = __float_as_uint(ex2(f2_hi(t)));
         }
-        const int valid = w.nv - u * 64;
+        const int valid = w.nv - w.j0 * 128 - u * 64;
         if (valid < 64) {
 #pragma unroll
           for (int c = 0; c < 64; ++c) s[c] = c < valid ? s[c] : 0u;
         }
-        if (T == 1) {
+        if (w.nv <= 64) {
           float d0 = 0.f, d1 = 0.f;
 #pragma unroll
           for (int c = 0; c < 64; c += 2) {
@@ -420,6 +420,28 @@ cross_dq_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
             break;
           }
           fence_after_sync();
+        }
+        if (W.splits > 1) {
+          // a share's sums, in 32 bits, for cross_sum_kernel
+          const int64_t rows = (int64_t)W.BH * W.Lq, flat = (int64_t)w.bh * W.Lq + row0 + lane;
+          float* dst = W.part + (w.split * rows + flat) * D;
+          const float f = w.T > 0 ? a.scale : 0.f;
+#pragma unroll 1
+          for (int ch = 0; ch < D / 32; ++ch) {
+            uint32_t o[32];
+            tmem_ld32(lane_base + OC + x * D + ch * 32, o);
+            tmem_wait_ld();
+            if (row0 + lane < W.Lq) {
+#pragma unroll
+              for (int e = 0; e < 32; e += 4)
+                put4(dst + ch * 32 + e, w.T > 0 ? __uint_as_float(o[e]) * f : 0.f,
+                     w.T > 0 ? __uint_as_float(o[e + 1]) * f : 0.f, w.T > 0 ? __uint_as_float(o[e + 2]) * f : 0.f,
+                     w.T > 0 ? __uint_as_float(o[e + 3]) * f : 0.f);
+            }
+          }
+          fence_before_sync();
+          if (w.T > 0) mbar_arrive(&o_empty[x]);
+          continue;
         }
         store_tile<D>(lane_base + OC + x * D, w.T > 0, a.scale, &o_empty[x], sStage + quarter * 4096,
                       a.dq + w.b * a.sdq.b + w.h * a.sdq.h + (int64_t)row0 * a.sdq.r, a.sdq.r, W.Lq - row0, lane);
@@ -500,7 +522,8 @@ struct CrossKeySpace {
       heads = 0;
       for (int b = 0; b < a.batch; ++b) heads += tiles(a, b);
       heads *= a.kv_heads;
-      ranges = min((int64_t)ctas, (heads * steps + 7) / 8);
+      const int least = min(8, steps);
+      ranges = min((int64_t)ctas, (heads * steps + least - 1) / least);
     }
   }
   __device__ __forceinline__ int64_t start(int64_t g) const { return g < ranges ? heads * steps * g / ranges : heads * steps; }
@@ -794,7 +817,7 @@ cross_dkv_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
   if (warp == 17) tmem_dealloc(tmem, 512);
 }
 
-// dv (blockIdx.y = 0) and dk (1): the pieces of each key row in CTA order, the
+// dv (blockIdx.z = 0) and dk (1): the pieces of each key row in CTA order, the
 // scale, the rounding, and zeros where the key was not allowed.  `place`: packed
 // row of each key (null: the key's own).
 struct CrossReduceArgs {
@@ -806,38 +829,66 @@ struct CrossReduceArgs {
   int ctas;
 };
 
+constexpr int kReduceKeys = 16;
+
+// Grid: (blocks of 16 keys, batch * kv_heads, dv / dk).  The packed rows of 16
+// keys lie in two key tiles at most; where the pieces of those begin and end
+// takes a few 64-bit divisions, which two threads do for the block.
 template <int D>
 __global__ void __launch_bounds__(256) cross_dkv_reduce_kernel(const CrossReduceArgs r) {
+  __shared__ int64_t slot0[2];
+  __shared__ int pieces[2], places[kReduceKeys], low;
   const CrossDkvArgs& a = r.a;
-  const int64_t flat = (int64_t)blockIdx.x * (256 / (D / 4)) + threadIdx.x / (D / 4);
-  if (flat >= (int64_t)a.batch * a.kv_heads * a.Lk) return;
-  const int c = threadIdx.x % (D / 4) * 4;
-  const int j = (int)(flat % a.Lk), bh = (int)(flat / a.Lk), b = bh / a.kv_heads, hk = bh % a.kv_heads;
-  const int at = r.place == nullptr ? j : r.place[(int64_t)b * a.Lk + j];
-  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (at >= 0) {
+  const int bh = blockIdx.y, b = bh / a.kv_heads, hk = bh % a.kv_heads, j0 = blockIdx.x * kReduceKeys;
+  if (threadIdx.x == 0) low = 0x7fffffff;
+  __syncthreads();
+  if (threadIdx.x < kReduceKeys) {
+    const int j = j0 + threadIdx.x;
+    const int at = j >= a.Lk ? -1 : r.place == nullptr ? j : r.place[(int64_t)b * a.Lk + j];
+    places[threadIdx.x] = at;
+    if (at >= 0) atomicMin(&low, at);
+  }
+  __syncthreads();
+  const int tile0 = low / 128;
+  if (threadIdx.x < 2 && low != 0x7fffffff) {
     const CrossKeySpace ks(a, r.ctas);
+    const int tile = tile0 + (int)threadIdx.x;
     int64_t item = bh;
+    int lane = tile;
     if (a.count != nullptr) {
       item = 0;
       for (int i = 0; i < b; ++i) item += CrossKeySpace::tiles(a, i);
-      item = item * a.kv_heads + hk * CrossKeySpace::tiles(a, b) + at / 128;
+      item = item * a.kv_heads + hk * CrossKeySpace::tiles(a, b) + tile;
+      lane = 0;
     }
-    const int64_t first = ks.owner(item * ks.steps), last = ks.owner((item + 1) * ks.steps - 1);
-    const int lane = a.count == nullptr ? at / 128 : 0;
-    for (int64_t g = first; g <= last; ++g) {
-      const float4 y = *reinterpret_cast<const float4*>(
-          a.part + ((ks.slot(item, g, lane) * 2 + blockIdx.y) * 128 + at % 128) * D + c);
-      x.x += y.x;
-      x.y += y.y;
-      x.z += y.z;
-      x.w += y.w;
+    if (tile < CrossKeySpace::tiles(a, b)) {
+      const int64_t first = ks.owner(item * ks.steps), last = ks.owner((item + 1) * ks.steps - 1);
+      slot0[threadIdx.x] = ks.slot(item, first, lane);
+      pieces[threadIdx.x] = (int)(last - first + 1);
     }
   }
-  const float f = blockIdx.y == 0 ? 1.f : r.scale;
-  const HeadView& st = blockIdx.y == 0 ? r.sdv : r.sdk;
-  put4((blockIdx.y == 0 ? r.dv : r.dk) + b * st.b + hk * st.h + (int64_t)j * st.r + c, x.x * f, x.y * f, x.z * f,
-       x.w * f);
+  __syncthreads();
+  const int c = threadIdx.x % (D / 4) * 4;
+  const float f = blockIdx.z == 0 ? 1.f : r.scale;
+  const HeadView& st = blockIdx.z == 0 ? r.sdv : r.sdk;
+  __nv_bfloat16* out = (blockIdx.z == 0 ? r.dv : r.dk) + b * st.b + hk * st.h + c;
+  for (int i = threadIdx.x / (D / 4); i < kReduceKeys && j0 + i < a.Lk; i += 256 / (D / 4)) {
+    const int at = places[i];
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (at >= 0) {
+      const int which = at / 128 - tile0;
+      const float* p = a.part + ((slot0[which] * 2 + blockIdx.z) * 128 + at % 128) * D + c;
+#pragma unroll 4
+      for (int s = 0; s < pieces[which]; ++s) {  // a lane's pieces of one item lie in consecutive slots
+        const float4 y = *reinterpret_cast<const float4*>(p + (int64_t)s * 2 * 128 * D);
+        x.x += y.x;
+        x.y += y.y;
+        x.z += y.z;
+        x.w += y.w;
+      }
+    }
+    put4(out + (int64_t)(j0 + i) * st.r, x.x * f, x.y * f, x.z * f, x.w * f);
+  }
 }
 
 }  // namespace pisa

@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(kCrossThreads) cross_fwd_simt_kernel(const Cro
 
 // Backward, queries: a CTA owns BM query rows and share blockIdx.z of their
 // keys; one pass over the keys in tiles of BN.  Writes dq and delta; splits > 1:
-// part [splits][batch * heads][Lq][D], added in order by cross_dq_sum_kernel.
+// part [splits][batch * heads][Lq][D], added in order by cross_sum_kernel.
 template <int D, int RI>
 struct CrossDqSimt {
   static constexpr int BM = 16 * RI, BN = D == 64 ? 64 : 32;
@@ -398,7 +398,7 @@ __global__ void __launch_bounds__(kCrossThreads) cross_dq_simt_kernel(const Cros
 // Backward, keys: a CTA owns 64 keys of one key head and a contiguous share
 // (blockIdx.z of `splits`) of the query tiles of all heads that read it, in
 // order; its sums go to dk and dv, or with splits > 1 to part [splits][2][batch
-// * kv_heads][Lk][D], which cross_dkv_sum_kernel adds in split order (no
+// * kv_heads][Lk][D], which cross_sum_kernel adds in split order (no
 // atomics: results do not depend on timing).
 template <int D>
 struct CrossDkvSimt {
@@ -497,13 +497,13 @@ __global__ void __launch_bounds__(kCrossThreads) cross_dkv_simt_kernel(const Cro
 struct CrossSumArgs {
   const float* part;
   int64_t rows, pitch;  // rows of one tensor, floats between two splits
-  float* out[2];
+  void* out[2];
   HeadView so[2];
   int heads, L, splits;
 };
 
 // Grid y: the tensors that lie next to each other in a split (dk and dv), or one.
-template <int D>
+template <typename T, int D>
 __global__ void __launch_bounds__(256) cross_sum_kernel(const CrossSumArgs a) {
   const int64_t e = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
   if (e >= a.rows * D) return;
@@ -520,7 +520,7 @@ __global__ void __launch_bounds__(256) cross_sum_kernel(const CrossSumArgs a) {
     x.w += y.w;
   }
   const HeadView& st = a.so[blockIdx.y];
-  put4(a.out[blockIdx.y] + b * st.b + h * st.h + (int64_t)i * st.r + c, x.x, x.y, x.z, x.w);
+  put4(static_cast<T*>(a.out[blockIdx.y]) + b * st.b + h * st.h + (int64_t)i * st.r + c, x.x, x.y, x.z, x.w);
 }
 
 // Joins the shares of a forward pass: out = sum_s w_s o_s / sum_s w_s with

@@ -74,15 +74,23 @@ __global__ void __launch_bounds__(kPackThreads) cross_pack_kernel(const CrossPac
   const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(a.k) + b * a.sk.b + hk * a.sk.h;
   const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.v) + b * a.sv.b + hk * a.sv.h;
   const int64_t out = ((int64_t)blockIdx.y * a.padded + first) * D;
-  for (int e = threadIdx.x; e < end * (D / 8); e += kPackThreads) {
-    const int r = e / (D / 8), c = e % (D / 8) * 8;
-    uint4 x = make_uint4(0, 0, 0, 0), y = x;
-    if (src[r] >= 0) {
-      x = *reinterpret_cast<const uint4*>(k + src[r] * a.sk.r + c);
-      y = *reinterpret_cast<const uint4*>(v + src[r] * a.sv.r + c);
+  constexpr int U = kPackRows * (D / 8) / kPackThreads;  // 16-byte units of a thread, all loads under way at once
+  uint4 x[U], y[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int e = threadIdx.x + u * kPackThreads, r = e / (D / 8), c = e % (D / 8) * 8;
+    x[u] = y[u] = make_uint4(0, 0, 0, 0);
+    if (r < end && src[r] >= 0) {
+      x[u] = *reinterpret_cast<const uint4*>(k + src[r] * a.sk.r + c);
+      y[u] = *reinterpret_cast<const uint4*>(v + src[r] * a.sv.r + c);
     }
-    *reinterpret_cast<uint4*>(a.pk + out + r * D + c) = x;
-    *reinterpret_cast<uint4*>(a.pv + out + r * D + c) = y;
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int e = threadIdx.x + u * kPackThreads, r = e / (D / 8), c = e % (D / 8) * 8;
+    if (r >= end) continue;
+    *reinterpret_cast<uint4*>(a.pk + out + r * D + c) = x[u];
+    *reinterpret_cast<uint4*>(a.pv + out + r * D + c) = y[u];
   }
 }
 
@@ -94,7 +102,8 @@ __global__ void __launch_bounds__(kPackThreads) cross_pack_kernel(const CrossPac
 // self-attention kernel: warps 0-3 / 4-7 softmax of tile A / B, a thread per
 // query row (= TMEM lane), warp 8 TMA producer, warp 9 MMA issuer, 10-11 idle.
 // S = Q K^T, then P (bf16, over S in TMEM) and O += P V; both tiles use each
-// key and value tile, loaded once into a ring of three 128-row slots.
+// key and value tile, loaded once into a ring of four 128-row slots (three left
+// the issuer waiting for keys in every second step).
 //
 // Text has few keys (4 tiles of 128 for 512), so an item is short and what
 // counts is that items follow each other without a gap: the issuer runs one
@@ -116,7 +125,7 @@ struct CrossFwdArgs {
   float scale_log2;
 };
 
-constexpr int kCrossStages = 3, kCrossFwdThreads = 384, kCrossFwdRegs = 168;
+constexpr int kCrossStages = 4, kCrossFwdThreads = 384, kCrossFwdRegs = 168;
 constexpr int kCrossThreads512 = 512, kCrossRegs512 = 128;
 
 // Registers of the four warpgroups: two of rows, producer / issuer, epilogue.
@@ -177,8 +186,9 @@ template <int D>
 struct CrossFwdLayout {
   static constexpr uint32_t kTile = 128u * D * 2u;
   static constexpr int kNumBars = 2 * kCrossStages + 11;
-  static constexpr size_t bytes() {  // Q and output of both tiles, the ring
-    return 1024 + (4 + kCrossStages) * kTile + kNumBars * 8 + 16;
+  static constexpr uint32_t kOut = 128u * 64u * 2u;  // 64 output columns of a tile
+  static constexpr size_t bytes() {
+    return 1024 + (2 + kCrossStages) * kTile + 2 * kOut + kNumBars * 8 + 16;
   }
 };
 
@@ -224,7 +234,7 @@ cross_fwd_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
   uint8_t* sQ = smem;
   uint8_t* sRing = smem + 2 * TILE;
   uint8_t* sOut = sRing + NS * TILE;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sOut + 2 * TILE);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sOut + 2 * Lay::kOut);
   uint64_t* empty = full + NS;
   uint64_t* q_full = empty + NS;    // [2]
   uint64_t* q_empty = q_full + 2;   // [2]
@@ -415,7 +425,7 @@ cross_fwd_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
     const float c2 = a.scale_log2;
     int steps = 0, outs = 0;
     bool ok = true;
-    uint8_t* stage = sOut + x * TILE + warp % 4 * (TILE / 4);  // this warp's 32 output rows
+    uint8_t* stage = sOut + x * Lay::kOut + warp % 4 * (Lay::kOut / 4);  // 64 columns of this warp's 32 output rows
     CrossItem w, nxt;
     nxt.at(a, blockIdx.x);
     for (int i = blockIdx.x; ok && i < a.n_items; i += gridDim.x) {
@@ -531,31 +541,31 @@ cross_fwd_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
         }
       } else {
         if (in && a.lse != nullptr) a.lse[flat] = lse2 * 0.6931471805599453f;
-        if (lane == 0) tma_store_wait_read();  // the last item's rows have left
-        __syncwarp();
 #pragma unroll 1
-        for (int ch = 0; ch < D / 32; ++ch) {
-          uint32_t o[32];
-          tmem_ld32(obase + ch * 32, o);  // without keys whatever is there: replaced
-          tmem_wait_ld();
-          uint8_t* to = stage + (ch >> 1) * 4096 + lane * 128;
+        for (int cb = 0; cb < CB; ++cb) {
+          uint32_t pk[32];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t pk[4];
+          for (int hh = 0; hh < 2; ++hh) {
+            uint32_t o[32];
+            tmem_ld32(obase + cb * 64 + hh * 32, o);  // without keys whatever is there: replaced
+            tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              pk[e] = w.T > 0 ? pack_bf16x2(__uint_as_float(o[8 * c + 2 * e]) * inv,
-                                            __uint_as_float(o[8 * c + 2 * e + 1]) * inv)
-                              : 0u;
-            *reinterpret_cast<uint4*>(to + ((((ch & 1) * 4 + c) ^ (lane & 7)) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+            for (int e = 0; e < 16; ++e)
+              pk[hh * 16 + e] = w.T > 0 ? pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv)
+                                        : 0u;
           }
-        }
-        fence_async_shared();
-        __syncwarp();
-        if (lane == 0 && row0 < a.Lq) {
+          if (lane == 0) tma_store_wait_read();  // what was in the buffer has left
+          __syncwarp();
 #pragma unroll
-          for (int cb = 0; cb < CB; ++cb) tma_store_4d(&tmO, stage + cb * 4096, cb * 64, row0, w.h, w.b);
-          tma_store_commit();
+          for (int c = 0; c < 8; ++c)
+            *reinterpret_cast<uint4*>(stage + lane * 128 + ((c ^ (lane & 7)) << 4)) =
+                make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+          fence_async_shared();
+          __syncwarp();
+          if (lane == 0 && row0 < a.Lq) {
+            tma_store_4d(&tmO, stage, cb * 64, row0, w.h, w.b);
+            tma_store_commit();
+          }
         }
       }
       fence_before_sync();  // before this tile's next P releases the P V that overwrites O

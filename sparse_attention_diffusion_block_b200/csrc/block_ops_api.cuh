@@ -81,13 +81,20 @@ bool rope_plan_ok(const pisa_rope_plan* p) {
 }
 
 // Tokens per block: as many as one step of its threads takes (whole pieces of
-// 4 KB on the [batch, heads, L, d] side), fewer where that gives less than 32
-// blocks per SM, four rounds of what is resident (9973 tokens, 96 heads: 96 us;
-// with eight blocks per SM 110, with four 133).
+// 4 KB on the [batch, heads, L, d] side); half as many, again and again, where
+// that leaves less than 32 blocks per SM, four rounds of what is resident (9973
+// tokens, 96 heads: 96 us; with eight blocks per SM 110, with four 133), as long
+// as each thread keeps eight rows to set its start against (27639 tokens, 4
+// heads: 23 us, with one row 43), unless SMs would have no block at all.
 template <typename T, bool HALF, int V>
 pisa_status launch_rope(RopeArgs a, int batch, cudaStream_t st) {
-  a.tokens = kRopeThreads / (a.d / (HALF ? 2 * V : V));
-  while (a.tokens > 1 && (long long)((a.L + a.tokens - 1) / a.tokens) * batch < 32LL * kSMs) a.tokens /= 2;
+  const int slots = kRopeThreads / (a.d / (HALF ? 2 * V : V)), rows = a.q.heads + a.k.heads;
+  a.tokens = slots;
+  while (a.tokens > 1) {
+    const long long blocks = (long long)((a.L + a.tokens - 1) / a.tokens) * batch;
+    if (blocks >= 32LL * kSMs || (blocks >= kSMs && rows * (a.tokens / 2) < 8 * slots)) break;
+    a.tokens /= 2;
+  }
   const size_t smem = (size_t)a.tokens * a.pairs * sizeof(float2);
   rope_kernel<T, HALF, V><<<dim3((a.L + a.tokens - 1) / a.tokens, batch), kRopeThreads, smem, st>>>(a);
   return last_launch();

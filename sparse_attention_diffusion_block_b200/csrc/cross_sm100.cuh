@@ -302,7 +302,14 @@ cross_fwd_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
           tma_load_4d(sQ + x * TILE + cb * 128 * 128, &tmQ, &q_full[x], cb * 64, (w.tile + x) * 128, w.h, w.b);
         ++nq[x];
       };
-      CrossItem cur, nxt;
+      // Queries come into L2 two items ahead: with one tile of keys an item is
+      // over before a read from memory would be back.
+      auto prefetch = [&](const CrossItem& w) {
+        for (int x = 0; x < w.tiles; ++x)
+#pragma unroll
+          for (int cb = 0; cb < CB; ++cb) tma_prefetch_4d(&tmQ, cb * 64, (w.tile + x) * 128, w.h, w.b);
+      };
+      CrossItem cur, nxt, far;
       int i = blockIdx.x;
       bool has = cur.with_keys(a, i);
       if (has) {
@@ -310,13 +317,13 @@ cross_fwd_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
         load(&tmK, cur, 0);
         load_q(cur, 1);
       }
+      i += gridDim.x;
+      bool more = has && nxt.with_keys(a, i);
+      if (more) prefetch(nxt);
       while (ok && has) {
         i += gridDim.x;
-        const bool more = nxt.with_keys(a, i);
-        if (more)
-          for (int x = 0; x < nxt.tiles; ++x)
-#pragma unroll
-            for (int cb = 0; cb < CB; ++cb) tma_prefetch_4d(&tmQ, cb * 64, (nxt.tile + x) * 128, nxt.h, nxt.b);
+        const bool third = more && far.with_keys(a, i);
+        if (third) prefetch(far);
         for (int u = 0; ok && u < cur.T; ++u) {
           load(&tmV, cur, u);
           if (u + 1 < cur.T) {
@@ -330,7 +337,9 @@ cross_fwd_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
           }
         }
         cur = nxt;
+        nxt = far;
         has = more;
+        more = third;
       }
       // the copies already issued land before the CTA can exit
       for (int u = it > NS ? it - NS : 0; u < it; ++u) mbar_drain(&full[u % NS], (u / NS) & 1);

@@ -88,10 +88,20 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
   const int b = blockIdx.y, t0 = blockIdx.x * a.tokens;
   const int here = min(a.tokens, a.L - t0);
   const float* pos = a.pos + b * a.pos_batch + (int64_t)t0 * a.axes;
+  // The argument arrays go through shared memory once: constant reads at a
+  // different index in each lane are served one by one, and reading them per
+  // angle kept that unit 81 % busy and the kernel from its bandwidth.
+  __shared__ double freq[kRopeMaxPairs];
+  __shared__ int axis[kRopeMaxPairs];
+  if ((int)threadIdx.x < a.pairs) {
+    freq[threadIdx.x] = a.freq[threadIdx.x];
+    axis[threadIdx.x] = a.axis[threadIdx.x];
+  }
+  __syncthreads();
   for (int e = threadIdx.x; e < here * a.pairs; e += kRopeThreads) {
     const int p = e % a.pairs;
     float s, c;
-    rope_angle((double)pos[e / a.pairs * a.axes + a.axis[p]], a.freq[p], &s, &c);
+    rope_angle((double)pos[e / a.pairs * a.axes + axis[p]], freq[p], &s, &c);
     rope_turns[e] = make_float2(c * a.magnitude, s * a.sign * a.magnitude);
   }
   __syncthreads();

@@ -427,8 +427,9 @@ pisa_status run_cross_fwd_sm100(const CrossArgs& a, const CrossShape& s, char* w
   int sms = 0;
   if (!sm_count(&sms)) return PISA_ERR_CUDA;
   const size_t smem = CrossFwdLayout<D>::bytes();
-  static const bool regs = launch_registers(cross_fwd_sm100_kernel<D>, kCrossFwdRegs);
-  if (!regs || !set_smem(cross_fwd_sm100_kernel<D>, smem)) return PISA_ERR_CUDA;
+  static std::atomic<bool> regs{false};  // only a good answer is kept
+  if (!regs && !(regs = launch_registers(cross_fwd_sm100_kernel<D>, kCrossFwdRegs))) return PISA_ERR_CUDA;
+  if (!set_smem(cross_fwd_sm100_kernel<D>, smem)) return PISA_ERR_CUDA;
   cross_fwd_sm100_kernel<D><<<f.n_items < sms ? f.n_items : sms, kCrossFwdThreads, smem, st>>>(mQ, mK, mV, mO, f);
   if (last_launch() != PISA_OK || p.splits == 1) return last_launch();
   return launch_cross_join<__nv_bfloat16, D>(a, s, p.splits, f.part, f.part_lse, st);
@@ -469,13 +470,14 @@ pisa_status launch_cross_rows(const CrossArgs& a, const CrossShape& s, cudaStrea
   if (cudaFuncSetAttribute(cross_rows_kernel<T, D, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ring) !=
       cudaSuccess)
     return PISA_ERR_CUDA;
-  static const int per_sm = [] {
+  static std::atomic<int> per_sm{0};
+  if (per_sm == 0) {
     int n = 0;
-    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, cross_rows_kernel<T, D, NQ>, kRowsThreads, ring) ==
-                   cudaSuccess && n > 0
-               ? n
-               : 1;
-  }();
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, cross_rows_kernel<T, D, NQ>, kRowsThreads, ring) !=
+            cudaSuccess || n < 1)
+      return PISA_ERR_CUDA;
+    per_sm = n;
+  }
   const long long slots = (long long)kSMs * per_sm;
   int x = 1;
   long long best = -1;
@@ -553,8 +555,9 @@ pisa_status run_cross_bwd_sm100(const CrossArgs& a, const CrossShape& s, char* w
   int sms = 0;
   if (!sm_count(&sms)) return PISA_ERR_CUDA;
   const size_t s1 = CrossDqLayout<D>::bytes(), s2 = CrossDkvLayout<D>::bytes();
-  static const bool regs = launch_registers(cross_dq_sm100_kernel<D>, kCrossRegs512);
-  if (!regs || !set_smem(cross_dq_sm100_kernel<D>, s1) || !set_smem(cross_dkv_sm100_kernel<D>, s2))
+  static std::atomic<bool> regs{false};
+  if (!regs && !(regs = launch_registers(cross_dq_sm100_kernel<D>, kCrossRegs512))) return PISA_ERR_CUDA;
+  if (!set_smem(cross_dq_sm100_kernel<D>, s1) || !set_smem(cross_dkv_sm100_kernel<D>, s2))
     return PISA_ERR_CUDA;
   cross_dq_sm100_kernel<D><<<f.w.n_items < sms ? f.w.n_items : sms, kCrossThreads512, s1, st>>>(q128, g128, k64, v64, f);
   if (last_launch() != PISA_OK) return PISA_ERR_CUDA;
@@ -572,7 +575,10 @@ pisa_status run_cross_bwd_sm100(const CrossArgs& a, const CrossShape& s, char* w
   r.ctas = p.splits;
   cross_dkv_sm100_kernel<D><<<p.splits, kDkvThreads, s2, st>>>(q64, g64, k128, v128, r.a);
   if (last_launch() != PISA_OK) return PISA_ERR_CUDA;
-  cross_dkv_reduce_kernel<D><<<dim3((s.Lk + kReduceKeys - 1) / kReduceKeys, s.batch * s.kv_heads, 2), 256, 0, st>>>(r);
+  // 16 keys a block while that leaves SMs room (333 keys of 16 key heads: 5.5 us,
+  // with 64 a block 8.9), 64 beyond eight blocks per SM (32768 of 4: 62 and 47 us)
+  r.keys = 2LL * s.batch * s.kv_heads * ((s.Lk + 15) / 16) <= 8LL * kSMs ? 16 : kReduceKeys;
+  cross_dkv_reduce_kernel<D><<<dim3((s.Lk + r.keys - 1) / r.keys, s.batch * s.kv_heads, 2), 256, 0, st>>>(r);
   return last_launch();
 }
 

@@ -826,23 +826,23 @@ struct CrossReduceArgs {
   __nv_bfloat16 *dk, *dv;
   HeadView sdk, sdv;
   float scale;
-  int ctas;
+  int ctas, keys;  // CTAs of the dk/dv kernel; keys per block here
 };
 
-constexpr int kReduceKeys = 16;
+constexpr int kReduceKeys = 64;  // most keys of a block
 
-// Grid: (blocks of 16 keys, batch * kv_heads, dv / dk).  The packed rows of 16
-// keys lie in two key tiles at most; where the pieces of those begin and end
+// Grid: (blocks of r.keys keys, batch * kv_heads, dv / dk).  The packed rows of
+// up to 64 keys lie in two key tiles at most; where the pieces of those begin and end
 // takes a few 64-bit divisions, which two threads do for the block.
 template <int D>
 __global__ void __launch_bounds__(256) cross_dkv_reduce_kernel(const CrossReduceArgs r) {
   __shared__ int64_t slot0[2];
   __shared__ int pieces[2], places[kReduceKeys], low;
   const CrossDkvArgs& a = r.a;
-  const int bh = blockIdx.y, b = bh / a.kv_heads, hk = bh % a.kv_heads, j0 = blockIdx.x * kReduceKeys;
+  const int bh = blockIdx.y, b = bh / a.kv_heads, hk = bh % a.kv_heads, j0 = blockIdx.x * r.keys;
   if (threadIdx.x == 0) low = 0x7fffffff;
   __syncthreads();
-  if (threadIdx.x < kReduceKeys) {
+  if ((int)threadIdx.x < r.keys) {
     const int j = j0 + threadIdx.x;
     const int at = j >= a.Lk ? -1 : r.place == nullptr ? j : r.place[(int64_t)b * a.Lk + j];
     places[threadIdx.x] = at;
@@ -872,7 +872,7 @@ __global__ void __launch_bounds__(256) cross_dkv_reduce_kernel(const CrossReduce
   const float f = blockIdx.z == 0 ? 1.f : r.scale;
   const HeadView& st = blockIdx.z == 0 ? r.sdv : r.sdk;
   __nv_bfloat16* out = (blockIdx.z == 0 ? r.dv : r.dk) + b * st.b + hk * st.h + c;
-  for (int i = threadIdx.x / (D / 4); i < kReduceKeys && j0 + i < a.Lk; i += 256 / (D / 4)) {
+  for (int i = threadIdx.x / (D / 4); i < r.keys && j0 + i < a.Lk; i += 256 / (D / 4)) {
     const int at = places[i];
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     if (at >= 0) {

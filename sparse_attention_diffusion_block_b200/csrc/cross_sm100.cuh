@@ -51,22 +51,45 @@ __global__ void __launch_bounds__(kPackThreads) cross_pack_kernel(const CrossPac
   } else {
     if (threadIdx.x < kPackRows) src[threadIdx.x] = -1;
     total = 0;
-    for (int j0 = 0; j0 < a.Lk; j0 += kPackThreads) {
-      const int j = j0 + threadIdx.x;
-      const bool on = j < len && mask[j] != 0;
-      const unsigned ballot = __ballot_sync(0xffffffffu, on);
+    // 16 keys a thread, 4096 a round
+    for (int j0 = 0; j0 < len; j0 += 16 * kPackThreads) {
+      const int j = j0 + 16 * (int)threadIdx.x;
+      unsigned bits = 0;
+      if (j + 16 <= len && (reinterpret_cast<uintptr_t>(mask + j) & 15) == 0) {
+        const uint4 raw = *reinterpret_cast<const uint4*>(mask + j);
+        const uint8_t* byte = reinterpret_cast<const uint8_t*>(&raw);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) bits |= (byte[e] != 0 ? 1u : 0u) << e;
+      } else {
+        for (int e = 0; e < 16; ++e)
+          if (j + e < len && mask[j + e] != 0) bits |= 1u << e;
+      }
+      const int mine = __popc(bits);
+      int upto = mine;  // in this warp, this thread's included
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += y;
+      }
       __syncthreads();
-      if (lane == 0) warp_sum[warp] = __popc(ballot);
+      if (lane == 31) warp_sum[warp] = upto;
       __syncthreads();
-      int before = total;
+      int at = total + upto - mine;
       for (int w = 0; w < kPackThreads / 32; ++w) {
-        if (w < warp) before += warp_sum[w];
+        if (w < warp) at += warp_sum[w];
         total += warp_sum[w];
       }
-      const int at = before + __popc(ballot & ((1u << lane) - 1u));
-      if (on && at >= first && at < first + kPackRows) src[at - first] = j;
-      if (report && a.place != nullptr && j < a.Lk) a.place[(int64_t)b * a.Lk + j] = on ? at : -1;
+      const bool here = at < first + kPackRows && at + mine > first;
+      if (here || (report && a.place != nullptr))
+        for (int e = 0; e < 16 && j + e < len; ++e) {
+          const bool on = (bits >> e) & 1u;
+          if (on && at >= first && at < first + kPackRows) src[at - first] = j + e;
+          if (report && a.place != nullptr) a.place[(int64_t)b * a.Lk + j + e] = on ? at : -1;
+          at += on;
+        }
     }
+    if (report && a.place != nullptr)
+      for (int j = len + (int)threadIdx.x; j < a.Lk; j += kPackThreads) a.place[(int64_t)b * a.Lk + j] = -1;
   }
   if (report && threadIdx.x == 0) a.count[b] = total;
   __syncthreads();

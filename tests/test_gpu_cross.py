@@ -204,6 +204,49 @@ def test_side_stream_two_graphs_and_workspace(lib, Lq, Lk, dtype):
         assert all(torch.equal(x, y) for x, y in zip(w, o))
 
 
+@pytest.mark.parametrize("Lk", [4095, 4097, 9000])
+@pytest.mark.parametrize("Lq", [1, 40])
+def test_long_masks(lib, Lq, Lk):
+    """Masks longer than one round of the packing, rows that start off a
+    16-byte boundary, and lengths on top."""
+    q, k, v, g = _make(12, 2, 2, 1, Lq, Lk, 64, torch.bfloat16)
+    gen = torch.Generator(device="cuda").manual_seed(13)
+    mask = torch.rand(2, Lk, device="cuda", generator=gen) < 0.3
+    mask[:, 1000:3000] = False
+    mask[0, -1] = True
+    _check(lib, q, k, v, g, key_mask=mask, what="mask")
+    _check(lib, q, k, v, g, key_mask=mask, kv_len=torch.tensor([Lk - 7, 17], dtype=torch.int32, device="cuda"),
+           what="mask and lengths")
+
+
+def test_offsets_past_32_bits(lib):
+    """17.5 million rows of 128: byte and element offsets past 2^32 and 2^31 in
+    queries, outputs and gradients; all but the last rows are zero."""
+    L = 17_500_000
+    q = torch.zeros(1, 1, L, 128, dtype=torch.bfloat16, device="cuda")
+    q[:, :, -3:] = _x(14, 1, 1, 3, 128)
+    k, v = _x(15, 1, 1, 70, 128), _x(16, 1, 1, 70, 128)
+    g = torch.zeros_like(q)
+    g[:, :, -3:] = _x(17, 1, 1, 3, 128)
+    ref = cross_ref(q[:, :, -3:], k, v, dout=g[:, :, -3:])
+    out, lse = lib.cross_attn_fwd(q, k, v, return_lse=True)
+    assert_within(out[:, :, -3:], ref["out"], "out")
+    dq, dk, dv = lib.cross_attn_bwd(g, q, k, v, out, lse)
+    assert_within(dq[:, :, -3:], ref["dq"], "dq")
+    # the other rows add p 0 = 0 to dv and ds q = 0 to dk; only their number enters the sums
+    assert_within(dk, ref["dk"], "dk")
+    assert_within(dv, ref["dv"], "dv")
+    pos = torch.arange(L, dtype=torch.float32, device="cuda")[:, None].contiguous()
+    far, _ = lib.rope(q, None, pos, (128,))
+    near, _ = lib.rope(q[:, :, -3:], None, pos[-3:].contiguous(), (128,))
+    assert torch.equal(far[:, :, -3:], near)
+    # as keys: the last row alone is allowed
+    mask = torch.zeros(1, L, dtype=torch.bool, device="cuda")
+    mask[0, -1] = True
+    one = lib.cross_attn_fwd(_x(18, 1, 1, 1, 128), q, q, key_mask=mask)
+    assert torch.equal(one, q[:, :, -1:])  # p = 1 exactly: the value itself
+
+
 def test_block_of_a_transformer(lib):
     """As a block calls them: rotary positions out of the fused projection, the
     piecewise sparse self-attention, cross-attention to padded text states, and

@@ -376,8 +376,8 @@ pisa_status pisa_rope_make_plan(int axes, const int* axis_dim, double theta, pis
  * reads), and may be the input itself with the same strides (in place); no
  * other overlap is allowed.  Pointers need only the element's alignment; where
  * pointers and strides are multiples of 16 bytes and the number of pairs is
- * one of the vector width (4 bf16 / 2 fp32 interleaved, 8 / 4 half), accesses
- * are 16 bytes wide.  positions: float32 [L, axes] shared by the batch
+ * one of 4 (of 2: interleaved fp32), accesses are 16 bytes wide (8: half bf16),
+ * otherwise single elements.  positions: float32 [L, axes] shared by the batch
  * (positions_batch_stride = 0), or one such table per batch entry at that
  * distance in elements.  backward != 0: q and k are output gradients, the
  * result is the input gradients (the transposed map).  Angles are formed in 64

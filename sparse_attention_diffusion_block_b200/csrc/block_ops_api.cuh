@@ -81,18 +81,19 @@ bool rope_plan_ok(const pisa_rope_plan* p) {
 }
 
 // Tokens per block: as many as one step of its threads takes (whole pieces of
-// 4 KB on the [batch, heads, L, d] side); half as many, again and again, where
-// that leaves less than 32 blocks per SM, four rounds of what is resident (9973
-// tokens, 96 heads: 96 us; with eight blocks per SM 110, with four 133), as long
-// as each thread keeps eight rows to set its start against (27639 tokens, 4
-// heads: 23 us, with one row 43), unless SMs would have no block at all.
+// 4 KB on the [batch, heads, L, d] side); half as many, again and again, up to 32
+// blocks per SM, four rounds of what is resident (9973 tokens, 96 heads: 96 us;
+// with eight blocks per SM 110, with four 133), as long as each thread keeps
+// eight rows to set its start against (27639 tokens, 4 heads: 23 us, with one row
+// 43), or two while SMs are not full (1000 tokens, 48 heads: 10 us, with 12 rows 14).
 template <typename T, bool HALF, int V>
 pisa_status launch_rope(RopeArgs a, int batch, cudaStream_t st) {
   const int slots = kRopeThreads / (a.d / (HALF ? 2 * V : V)), rows = a.q.heads + a.k.heads;
   a.tokens = slots;
   while (a.tokens > 1) {
     const long long blocks = (long long)((a.L + a.tokens - 1) / a.tokens) * batch;
-    if (blocks >= 32LL * kSMs || (blocks >= kSMs && rows * (a.tokens / 2) < 8 * slots)) break;
+    const int least = blocks < kSMs ? 0 : blocks < 8LL * kSMs ? 2 : 8;
+    if (blocks >= 32LL * kSMs || rows * (a.tokens / 2) < least * slots) break;
     a.tokens /= 2;
   }
   const size_t smem = (size_t)a.tokens * a.pairs * sizeof(float2);
@@ -100,12 +101,15 @@ pisa_status launch_rope(RopeArgs a, int batch, cudaStream_t st) {
   return last_launch();
 }
 
-// V: 16 bytes where every access is aligned and no unit mixes turned and
-// copied elements, one pair otherwise.
+// V: where every access is aligned and no unit mixes turned and copied
+// elements, 16 bytes; in the half layout a bf16 thread takes two runs of 8 bytes
+// instead (with two of 16 it holds 32 values and their 16 sines: 96.6 against
+// 93.0 us for 9973 tokens of 96 heads; fp32 gains from 16, 247 against 260 us for
+// 32760 tokens of 48).  One pair otherwise.
 template <typename T>
 pisa_status run_rope(const RopeArgs& a, bool half, bool wide, int batch, cudaStream_t st) {
   constexpr int W = 16 / sizeof(T);
-  if (half) return wide ? launch_rope<T, true, W>(a, batch, st) : launch_rope<T, true, 1>(a, batch, st);
+  if (half) return wide ? launch_rope<T, true, 4>(a, batch, st) : launch_rope<T, true, 1>(a, batch, st);
   return wide ? launch_rope<T, false, W>(a, batch, st) : launch_rope<T, false, 2>(a, batch, st);
 }
 
@@ -123,7 +127,7 @@ pisa_status rope_api(const void* q, void* q_out, const void* k, void* k_out, pis
   if (positions_batch_stride < 0 || positions_batch_stride > (1LL << 38)) return PISA_ERR_INVALID_ARG;
   const void* ptr[4] = {q, q_out, k, k_out};
   HeadView v[4];
-  bool wide = plan->pairs % (plan->layout == PISA_ROPE_HALF ? 16 / es : 8 / es) == 0;
+  bool wide = plan->pairs % (plan->layout == PISA_ROPE_HALF ? 4 : 8 / es) == 0;
   for (int i = 0; i < (k == nullptr ? 2 : 4); ++i) {
     v[i] = view_of(strides == nullptr ? nullptr : strides + i, batch, i < 2 ? heads : hk, L, d);
     if (!aligned_to(ptr[i], es) || !strides_in_range(v[i], d)) return PISA_ERR_INVALID_ARG;
@@ -266,8 +270,8 @@ struct CrossBwdPlan {
   size_t delta, part, total;
 };
 
-// fp32: query shares per key tile, enough CTAs for two per SM, at least two
-// query tiles each, and partials of at most 256 MB.  bf16: one CTA per SM, but
+// fp32: query shares per key tile, enough CTAs for two per SM, at least one
+// query tile each, and partials of at most 256 MB.  bf16: one CTA per SM, but
 // at least eight steps of 64 query rows each, or one key tile's where it has fewer.
 CrossBwdPlan cross_bwd_plan(const CrossShape& s) {
   CrossBwdPlan p{};
@@ -291,7 +295,7 @@ CrossBwdPlan cross_bwd_plan(const CrossShape& s) {
     const long long ctas = slices * ((s.Lk + 63) / 64), tiles = group * ((s.Lq + bq - 1) / bq);
     const long long one = 2LL * slices * s.Lk * s.d * sizeof(float);
     long long n = (2LL * kSMs + ctas - 1) / ctas;
-    if (n > tiles / 2) n = tiles / 2;
+    if (n > tiles) n = tiles;
     if (n > (256LL << 20) / one) n = (256LL << 20) / one;
     p.splits = (int)(n < 1 ? 1 : n);
     p.dq_splits = cross_simt_splits(s, bq);

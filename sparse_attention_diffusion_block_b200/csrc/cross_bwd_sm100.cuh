@@ -20,11 +20,13 @@ __device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
 
 // ------------------------------------------------------------------ delta
 //
-// delta_i = g_i . o_i: D / 8 lanes per row, four rows of a lane in flight.
+// delta_i = g_i . o_i: D / 8 lanes per row, two rows of a lane in flight
+// (more registers cost occupancy: 113 us for 32760 rows of 40 heads, four rows
+// 131, eight 218).
 // Reads both once, bound by HBM.  (Inside the dq kernel two spare warps could
 // not read ahead fast enough, 64 KB a tile: 1.75 ms instead of 0.65 + 0.1 for
 // 32760 rows of 40 heads.)  Grid: (rows of one head, batch * heads).
-constexpr int kDeltaRows = 4;
+constexpr int kDeltaRows = 2;
 
 struct CrossDeltaArgs {
   const __nv_bfloat16 *g, *o;

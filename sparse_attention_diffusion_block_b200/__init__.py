@@ -438,15 +438,15 @@ class _LaunchOn:
 
 
 def _same_kind(first: torch.Tensor, *others: Optional[torch.Tensor]) -> None:
-    dtype, device = first.dtype, first.device
-    if device.type != "cuda":
+    dtype, device = first.dtype, first.get_device()
+    if not first.is_cuda:
         raise ValueError("tensors must be CUDA tensors")
     for t in (first,) + others:
         if t is None:
             continue
         if t.dim() != 4 or t.stride(3) != 1 and t.shape[3] != 1:
             raise ValueError("tensors must be 4-d with a contiguous last dimension")
-        if t.dtype != dtype or t.device != device:
+        if t.dtype != dtype or t.get_device() != device:
             raise ValueError("tensors must share one dtype and one device")
 
 

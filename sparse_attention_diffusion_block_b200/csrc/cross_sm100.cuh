@@ -123,22 +123,27 @@ __global__ void __launch_bounds__(kPackThreads) cross_pack_kernel(const CrossPac
 // tiles (A, B) of one head, and, where there are fewer pairs than SMs, one of
 // `splits` shares of that head's key tiles.  Warp roles as in the fused
 // self-attention kernel: warps 0-3 / 4-7 softmax of tile A / B, a thread per
-// query row (= TMEM lane), warp 8 TMA producer, warp 9 MMA issuer, 10-11 idle.
-// S = Q K^T, then P (bf16, over S in TMEM) and O += P V; both tiles use each
-// key and value tile, loaded once into a ring of four 128-row slots (three left
-// the issuer waiting for keys in every second step).
+// query row (= TMEM lane), warp 8 TMA producer; warp 9 issues the MMAs of the
+// scores, warp 10 those of the output (11 idle).  S = Q K^T, then P (bf16) and O += P V; both tiles
+// use each key and value tile, loaded once.
 //
-// Text has few keys (4 tiles of 128 for 512), so an item is short and what
-// counts is that items follow each other without a gap: the issuer runs one
-// item's last P V and the next item's first Q K^T back to back, the next Q
-// tiles are in L2 by then, and outputs leave by TMA from shared memory of their
-// own while the softmax goes on.  75600 x 512, 40 heads of 128: 1.19 ms with
-// 16-byte stores of each thread's row, 0.85 ms with whole lines through shared
-// memory, which still held the softmax warps up for 3400 of 18100 cycles an
-// item.  (Four more warps for the epilogue took registers from the softmax and
-// the issuer: 1.13 ms.)
+// The two tiles share one S buffer: a softmax warpgroup copies its scores to
+// registers and hands the buffer on at once, so the next tile's scores are
+// formed while the exponentials run, and P has columns of its own.  Scores run
+// ahead of the products with V by a step; neither issuer waits for the other,
+// and one's commits and waits (80 to 190 cycles each) pass under the other's
+// MMAs.  (With P over S and one issuer a step of both tiles took 3400 cycles,
+// 2048 of them MMA: 0.76 ms for 75600 x 512, 40 heads of 128.)
 //
-// TMEM columns: [0,128) S_A, [128,256) S_B, [256,256+D) O_A, [256+D,256+2D) O_B.
+// Text has few keys (4 tiles of 128 for 512), so items are short and follow each
+// other without a gap: the next item's scores and exponentials come before this
+// one's output is read, the next Q tiles are in L2 by then, and outputs leave by
+// TMA from shared memory of their own.  On the way: 1.19 ms with 16-byte stores
+// of each thread's row, 0.85 ms with whole lines through shared memory; four
+// more warps for the epilogue took registers from the softmax and the issuer
+// (1.13 ms).
+//
+// TMEM columns: [0,128) S, [128,192) P_A, [192,256) P_B, [256,256+D) O_A, [256+D,256+2D) O_B.
 struct CrossFwdArgs {
   float* lse;            // [batch * heads][Lq] or null
   const int32_t* count;  // allowed keys per batch entry, or null: Lk
@@ -148,7 +153,7 @@ struct CrossFwdArgs {
   float scale_log2;
 };
 
-constexpr int kCrossStages = 4, kCrossFwdThreads = 384, kCrossFwdRegs = 168;
+constexpr int kCrossStages = 2, kCrossFwdThreads = 384, kCrossFwdRegs = 168;  // slots of each of K, V
 constexpr int kCrossThreads512 = 512, kCrossRegs512 = 128;
 
 // Registers of the four warpgroups: two of rows, producer / issuer, epilogue.
@@ -208,10 +213,10 @@ __device__ __forceinline__ void store_tile(uint32_t obase, bool work, float f, u
 template <int D>
 struct CrossFwdLayout {
   static constexpr uint32_t kTile = 128u * D * 2u;
-  static constexpr int kNumBars = 2 * kCrossStages + 11;
+  static constexpr int kNumBars = 4 * kCrossStages + 13;
   static constexpr uint32_t kOut = 128u * 64u * 2u;  // 64 output columns of a tile
   static constexpr size_t bytes() {
-    return 1024 + (2 + kCrossStages) * kTile + 2 * kOut + kNumBars * 8 + 16;
+    return 1024 + (2 + 2 * kCrossStages) * kTile + 2 * kOut + kNumBars * 8 + 16;
   }
 };
 
@@ -250,38 +255,40 @@ cross_fwd_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
   using namespace sm100;
   using Lay = CrossFwdLayout<D>;
   constexpr int CB = D / 64, NS = kCrossStages;
-  constexpr uint32_t TILE = Lay::kTile, OC = 256;
+  constexpr uint32_t TILE = Lay::kTile, PC = 128, OC = 256;
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;
-  uint8_t* sRing = smem + 2 * TILE;
-  uint8_t* sOut = sRing + NS * TILE;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sOut + 2 * Lay::kOut);
-  uint64_t* empty = full + NS;
-  uint64_t* q_full = empty + NS;    // [2]
+  uint8_t* sK = smem + 2 * TILE;
+  uint8_t* sV = sK + NS * TILE;
+  uint8_t* sOut = sV + NS * TILE;
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(sOut + 2 * Lay::kOut);
+  uint64_t* k_empty = k_full + NS;
+  uint64_t* v_full = k_empty + NS;
+  uint64_t* v_empty = v_full + NS;
+  uint64_t* q_full = v_empty + NS;  // [2]
   uint64_t* q_empty = q_full + 2;   // [2]
   uint64_t* s_full = q_empty + 2;   // [2]
-  uint64_t* p_full = s_full + 2;    // [2]
-  uint64_t* o_full = p_full + 2;    // [2]
-  uint64_t* mma_idle = o_full + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(full + Lay::kNumBars);
+  uint64_t* s_free = s_full + 2;
+  uint64_t* p_full = s_free + 1;    // [2]
+  uint64_t* pv_done = p_full + 2;   // [2]
+  uint64_t* mma_idle = pv_done + 2; // [2]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(k_full + Lay::kNumBars);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < NS; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
-    }
+    for (int s = 0; s < 4 * NS; ++s) mbar_init(&k_full[s], 1);  // k_full .. v_empty
     for (int x = 0; x < 2; ++x) {
       mbar_init(&q_full[x], 1);
       mbar_init(&q_empty[x], 1);
       mbar_init(&s_full[x], 1);
       mbar_init(&p_full[x], 128);
-      mbar_init(&o_full[x], 1);
+      mbar_init(&pv_done[x], 1);
+      mbar_init(&mma_idle[x], 1);
     }
-    mbar_init(mma_idle, 1);
+    mbar_init(s_free, 128);
     *abort = 0;
     fence_mbar_init();
   }
@@ -303,20 +310,23 @@ cross_fwd_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       prefetch_tensormap(&tmQ);
       prefetch_tensormap(&tmK);
       prefetch_tensormap(&tmV);
-      int it = 0, nq[2] = {0, 0};  // ring items and Q tiles loaded
+      int nk = 0, nv = 0, nq[2] = {0, 0};  // K, V and Q tiles loaded
       bool ok = true;
       const bool packed = a.count != nullptr;
-      auto load = [&](const CUtensorMap* map, const CrossItem& w, int j) {
-        const int s = it % NS;
-        if (!(ok = ok && mbar_wait(&empty[s], ((it / NS) & 1) ^ 1, abort))) return;
+      auto load = [&](const CUtensorMap* map, uint8_t* ring, uint64_t* full, uint64_t* empty, int& n, const CrossItem& w,
+                      int j) {
+        const int s = n % NS;
+        if (!(ok = ok && mbar_wait(&empty[s], ((n / NS) & 1) ^ 1, abort))) return;
         mbar_expect_tx(&full[s], TILE);
-        const int kh = w.bh / a.heads * a.kv_heads + w.hk;
+        const int kh = w.b * a.kv_heads + w.hk;
 #pragma unroll
         for (int cb = 0; cb < CB; ++cb)
-          tma_load_4d(sRing + s * TILE + cb * 128 * 128, map, &full[s], cb * 64, (w.j0 + j) * 128,
-                      packed ? kh : w.hk, packed ? 0 : w.b);
-        ++it;
+          tma_load_4d(ring + s * TILE + cb * 128 * 128, map, &full[s], cb * 64, (w.j0 + j) * 128, packed ? kh : w.hk,
+                      packed ? 0 : w.b);
+        ++n;
       };
+      auto load_k = [&](const CrossItem& w, int j) { load(&tmK, sK, k_full, k_empty, nk, w, j); };
+      auto load_v = [&](const CrossItem& w, int j) { load(&tmV, sV, v_full, v_empty, nv, w, j); };
       auto load_q = [&](const CrossItem& w, int x) {
         if (x >= w.tiles || !(ok = ok && mbar_wait(&q_empty[x], (nq[x] & 1) ^ 1, abort))) return;
         mbar_expect_tx(&q_full[x], TILE);
@@ -337,7 +347,7 @@ cross_fwd_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       bool has = cur.with_keys(a, i);
       if (has) {
         load_q(cur, 0);
-        load(&tmK, cur, 0);
+        load_k(cur, 0);
         load_q(cur, 1);
       }
       i += gridDim.x;
@@ -348,13 +358,14 @@ cross_fwd_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
         const bool third = more && far.with_keys(a, i);
         if (third) prefetch(far);
         for (int u = 0; ok && u < cur.T; ++u) {
-          load(&tmV, cur, u);
-          if (u + 1 < cur.T) {
-            load(&tmK, cur, u + 1);
-          } else if (more) {
-            // the tiles' buffers are free after their last S, one step before
-            // the next item's first
-            load(&tmK, nxt, 0);
+          // scores run a step ahead of the products with V
+          if (u + 1 < cur.T)
+            load_k(cur, u + 1);
+          else if (more)
+            load_k(nxt, 0);
+          load_v(cur, u);
+          if (u + 1 == cur.T && more) {
+            // free after the tiles' last S
             load_q(nxt, 0);
             load_q(nxt, 1);
           }
@@ -365,87 +376,71 @@ cross_fwd_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
         more = third;
       }
       // the copies already issued land before the CTA can exit
-      for (int u = it > NS ? it - NS : 0; u < it; ++u) mbar_drain(&full[u % NS], (u / NS) & 1);
+      for (int u = nk > NS ? nk - NS : 0; u < nk; ++u) mbar_drain(&k_full[u % NS], (u / NS) & 1);
+      for (int u = nv > NS ? nv - NS : 0; u < nv; ++u) mbar_drain(&v_full[u % NS], (u / NS) & 1);
       for (int x = 0; x < 2; ++x)
         if (nq[x] > 0) mbar_drain(&q_full[x], (nq[x] - 1) & 1);
     }
     __syncwarp();
    } else if (warp == 9) {
-    // ================================================================ MMA issuer
+    // ================================================================ issuer of S = Q K^T
     // The whole warp runs the loop (warp-uniform operands); one elected lane
     // issues each tcgen05 instruction.
     constexpr uint32_t idS = idesc_bf16(128, 128, false, false);
-    constexpr uint32_t idO = idesc_bf16(128, D, false, true);
-    const uint32_t ring = smem_u32(sRing), qbase = smem_u32(sQ);
-    int it = 0, steps[2] = {0, 0}, nq[2] = {0, 0};
+    const uint32_t ring = smem_u32(sK), qbase = smem_u32(sQ);
+    int n = 0, tiles = 0, nq[2] = {0, 0};
     bool ok = true;
-    auto take = [&](int& s) {
-      s = it % NS;
-      if (!(ok = ok && mbar_wait(&full[s], (it / NS) & 1, abort))) return;
-      fence_after_sync();
-      ++it;
-    };
-    // S_x = Q K^T; first / last: of the tile's item
-    auto s_mmas = [&](int x, int ks, bool first, bool last) {
-      if (first) {
-        if (!(ok = ok && mbar_wait(&q_full[x], nq[x] & 1, abort))) return;
-        ++nq[x];
-        fence_after_sync();
-      }
-      const uint32_t qb = qbase + x * TILE, kb = ring + ks * TILE;
+    CrossItem w;
+    for (int i = blockIdx.x; ok && w.with_keys(a, i); i += gridDim.x) {
+      for (int u = 0; ok && u < w.T; ++u, ++n) {
+        const uint32_t kb = ring + n % NS * TILE;
+        if (!(ok = mbar_wait(&k_full[n % NS], (n / NS) & 1, abort))) break;
+        for (int x = 0; x < w.tiles; ++x, ++tiles) {
+          if (u == 0 && !(ok = mbar_wait(&q_full[x], nq[x]++ & 1, abort))) break;
+          // the tile before has been read out of S
+          if (tiles > 0 && !(ok = mbar_wait(s_free, (tiles - 1) & 1, abort))) break;
+          fence_after_sync();
+          const uint32_t qb = qbase + x * TILE;
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        const uint32_t off = (kk >> 2) * 128 * 128 + (kk & 3) * 32;
-        mma_ss_warp(tmem + x * 128, desc_sw128(qb + off, 16, 1024), desc_sw128(kb + off, 16, 1024), idS,
-                    kk > 0 ? 1u : 0u);
-      }
-      mma_commit_warp(&s_full[x]);
-      if (last) mma_commit_warp(&q_empty[x]);
-    };
-    CrossItem cur, nxt;
-    int i = blockIdx.x, ks = 0, vs = 0;
-    bool has = cur.with_keys(a, i);
-    if (has) {
-      take(ks);
-      for (int x = 0; ok && x < cur.tiles; ++x) s_mmas(x, ks, true, cur.T == 1);
-      if (ok) mma_commit_warp(&empty[ks]);
-    }
-    while (ok && has) {
-      i += gridDim.x;
-      const bool more = nxt.with_keys(a, i);
-      for (int u = 0; ok && u < cur.T; ++u) {
-        const bool last = u + 1 == cur.T;
-        const bool next = !last || more;  // S tiles follow
-        take(vs);
-        if (ok && next) take(ks);
-        for (int x = 0; ok && x < 2; ++x) {
-          if (x < cur.tiles) {
-            if (!(ok = mbar_wait(&p_full[x], steps[x] & 1, abort))) break;
-            ++steps[x];
-            fence_after_sync();
-            const uint32_t vb = ring + vs * TILE;
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              mma_ts_warp(tmem + OC + x * D, tmem + x * 128 + kk * 8, desc_sw128(vb + kk * 16 * 128, 128 * 128, 1024),
-                          idO, (u > 0 || kk > 0) ? 1u : 0u);
-            if (last) mma_commit_warp(&o_full[x]);
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk >> 2) * 128 * 128 + (kk & 3) * 32;
+            mma_ss_warp(tmem, desc_sw128(qb + off, 16, 1024), desc_sw128(kb + off, 16, 1024), idS, kk > 0 ? 1u : 0u);
           }
-          if (!last) {
-            if (x < cur.tiles) s_mmas(x, ks, false, u + 2 == cur.T);
-          } else if (more && x < nxt.tiles) {
-            s_mmas(x, ks, true, nxt.T == 1);
-          }
+          mma_commit_warp(&s_full[x]);
+          if (u + 1 == w.T) mma_commit_warp(&q_empty[x]);
         }
-        if (!ok) break;
-        mma_commit_warp(&empty[vs]);
-        if (next) mma_commit_warp(&empty[ks]);
+        if (ok) mma_commit_warp(&k_empty[n % NS]);
       }
-      cur = nxt;
-      has = more;
     }
     // every MMA issued completes before TMEM is freed
-    mma_commit_warp(mma_idle);
-    mbar_drain(mma_idle, 0);
+    mma_commit_warp(&mma_idle[0]);
+    mbar_drain(&mma_idle[0], 0);
+    __syncwarp();
+   } else if (warp == 10) {
+    // ================================================================ issuer of O += P V
+    constexpr uint32_t idO = idesc_bf16(128, D, false, true);
+    const uint32_t ring = smem_u32(sV);
+    int n = 0, steps[2] = {0, 0};
+    bool ok = true;
+    CrossItem w;
+    for (int i = blockIdx.x; ok && w.with_keys(a, i); i += gridDim.x) {
+      for (int u = 0; ok && u < w.T; ++u, ++n) {
+        const uint32_t vb = ring + n % NS * TILE;
+        if (!(ok = mbar_wait(&v_full[n % NS], (n / NS) & 1, abort))) break;
+        for (int x = 0; x < w.tiles; ++x) {
+          if (!(ok = mbar_wait(&p_full[x], steps[x]++ & 1, abort))) break;
+          fence_after_sync();
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            mma_ts_warp(tmem + OC + x * D, tmem + PC + x * 64 + kk * 8, desc_sw128(vb + kk * 16 * 128, 128 * 128, 1024),
+                        idO, (u > 0 || kk > 0) ? 1u : 0u);
+          mma_commit_warp(&pv_done[x]);
+        }
+        if (ok) mma_commit_warp(&v_empty[n % NS]);
+      }
+    }
+    mma_commit_warp(&mma_idle[1]);
+    mbar_drain(&mma_idle[1], 0);
     __syncwarp();
    }
   } else {
@@ -453,18 +448,72 @@ cross_fwd_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
     // ================================================================ softmax: tile A (warps 0-3), B (4-7)
     const int x = warp / 4;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp % 4) * 32) << 16);
-    const uint32_t sbase = lane_base + x * 128, obase = lane_base + OC + x * D;
+    const uint32_t pbase = lane_base + PC + x * 64, obase = lane_base + OC + x * D;
     const float c2 = a.scale_log2;
-    int steps = 0, outs = 0;
-    bool ok = true;
     uint8_t* stage = sOut + x * Lay::kOut + warp % 4 * (Lay::kOut / 4);  // 64 columns of this warp's 32 output rows
-    CrossItem w, nxt;
-    nxt.at(a, blockIdx.x);
+    // o = O / l (0 without keys) of an item whose products are done
+    auto finish = [&](const CrossItem& w, float m, float l) {
+      const int row0 = (w.tile + x) * 128 + warp % 4 * 32, qrow = row0 + lane;
+      const bool in = qrow < a.Lq;
+      const float inv = w.T > 0 ? 1.f / l : 0.f;
+      const float lse2 = w.T > 0 ? m + log2f(l) : -INFINITY;
+      const int64_t flat = (int64_t)w.bh * a.Lq + qrow;
+      if (a.splits > 1) {
+        const int64_t at = (int64_t)w.split * a.BH * a.Lq + flat;
+        if (in) a.part_lse[at] = lse2;
+        if (w.T == 0) return;  // weight zero: the share's output is not read
+#pragma unroll 1
+        for (int ch = 0; ch < D / 32; ++ch) {
+          uint32_t o[32];
+          tmem_ld32(obase + ch * 32, o);
+          tmem_wait_ld();
+          if (in) {
+            float4* dst = reinterpret_cast<float4*>(a.part + at * D + ch * 32);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              dst[e] = make_float4(__uint_as_float(o[4 * e]) * inv, __uint_as_float(o[4 * e + 1]) * inv,
+                                   __uint_as_float(o[4 * e + 2]) * inv, __uint_as_float(o[4 * e + 3]) * inv);
+          }
+        }
+        return;
+      }
+      if (in && a.lse != nullptr) a.lse[flat] = lse2 * 0.6931471805599453f;
+#pragma unroll 1
+      for (int cb = 0; cb < CB; ++cb) {
+        uint32_t pk[32];
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          uint32_t o[32];
+          tmem_ld32(obase + cb * 64 + hh * 32, o);  // without keys whatever is there: replaced
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            pk[hh * 16 + e] = w.T > 0 ? pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv)
+                                      : 0u;
+        }
+        if (lane == 0) tma_store_wait_read();  // what was in the buffer has left
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          *reinterpret_cast<uint4*>(stage + lane * 128 + ((c ^ (lane & 7)) << 4)) =
+              make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0 && row0 < a.Lq) {
+          tma_store_4d(&tmO, stage, cb * 64, row0, w.h, w.b);
+          tma_store_commit();
+        }
+      }
+    };
+    int steps = 0;
+    bool ok = true, open = false;  // open: the item before is not finished yet
+    CrossItem w, last;
+    float last_m = 0.f, last_l = 1.f;
     for (int i = blockIdx.x; ok && i < a.n_items; i += gridDim.x) {
-      w = nxt;
-      const bool more = i + (int)gridDim.x < a.n_items;
-      if (x >= w.tiles) {
-        if (more) nxt.at(a, i + gridDim.x);
+      w.at(a, i);
+      if (x >= w.tiles) continue;
+      if (w.T == 0) {
+        finish(w, 0.f, 1.f);
         continue;
       }
       float m = -INFINITY, l = 0.f;
@@ -474,13 +523,14 @@ cross_fwd_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
           ok = false;
           break;
         }
-        ++steps;
         fence_after_sync();
-        tmem_ld32(sbase, s);
-        tmem_ld32(sbase + 32, s + 32);
-        tmem_ld32(sbase + 64, s + 64);
-        tmem_ld32(sbase + 96, s + 96);
+        tmem_ld32(lane_base, s);
+        tmem_ld32(lane_base + 32, s + 32);
+        tmem_ld32(lane_base + 64, s + 64);
+        tmem_ld32(lane_base + 96, s + 96);
         tmem_wait_ld();
+        fence_before_sync();
+        mbar_arrive(s_free);  // the next tile's scores may come
         const int valid = w.nv - (w.j0 + u) * 128;
         if (valid < 128) {
 #pragma unroll
@@ -505,8 +555,28 @@ cross_fwd_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
           }
           m = m_new;
         }
-        // O is quiescent: this S was issued after the tile's last P V
-        if (__any_sync(0xffffffffu, f != 1.f)) {
+        const float mu = m == -INFINITY ? 0.f : m;
+        const uint64_t c2x2 = f2_pack(c2, c2), nmu = f2_pack(-mu, -mu);
+        uint64_t acc = 0;
+#pragma unroll
+        for (int c = 0; c < 128; c += 2) {
+          const uint64_t t = ffma2(f2_pack(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), c2x2, nmu);
+          const float p0 = ex2(f2_lo(t)), p1 = ex2(f2_hi(t));
+          acc = fadd2(acc, f2_pack(p0, p1));
+          s[c >> 1] = pack_bf16x2(p0, p1);  // the product's operand type; the sum keeps 32 bits
+        }
+        l += f2_lo(acc) + f2_hi(acc);
+        // the tile's products so far are done: its P columns are free, and O
+        // is quiescent
+        if (steps > 0 && !__all_sync(0xffffffffu, mbar_wait(&pv_done[x], (steps - 1) & 1, abort))) {
+          ok = false;
+          break;
+        }
+        ++steps;
+        fence_after_sync();
+        if (u == 0) {
+          if (open) finish(last, last_m, last_l);
+        } else if (__any_sync(0xffffffffu, f != 1.f)) {
           uint32_t o[32];
 #pragma unroll 1
           for (int ch = 0; ch < D / 32; ++ch) {
@@ -516,91 +586,21 @@ cross_fwd_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
             for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
             tmem_st32(obase + ch * 32, o);
           }
-          tmem_wait_st();
         }
-        const float mu = m == -INFINITY ? 0.f : m;
-        const uint64_t c2x2 = f2_pack(c2, c2), nmu = f2_pack(-mu, -mu);
-        uint64_t acc = 0;
-#pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-#pragma unroll
-          for (int c = hh * 64; c < hh * 64 + 64; c += 2) {
-            const uint64_t t = ffma2(f2_pack(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), c2x2, nmu);
-            const float p0 = ex2(f2_lo(t)), p1 = ex2(f2_hi(t));
-            acc = fadd2(acc, f2_pack(p0, p1));
-            s[c >> 1] = pack_bf16x2(p0, p1);  // the product's operand type; the sum keeps 32 bits
-          }
-          if (hh == 0) tmem_st32(sbase, s);
-        }
-        l += f2_lo(acc) + f2_hi(acc);
-        tmem_st32(sbase + 32, s + 32);
+        tmem_st32(pbase, s);
+        tmem_st32(pbase + 32, s + 32);
         tmem_wait_st();
         fence_before_sync();
         mbar_arrive(&p_full[x]);
       }
-      if (!ok) break;
-      if (more) nxt.at(a, i + gridDim.x);  // its divisions run while P V does
-      // epilogue: o = O / l (0 without keys)
-      const int row0 = (w.tile + x) * 128 + warp % 4 * 32, qrow = row0 + lane;
-      const bool in = qrow < a.Lq;
-      const float inv = w.T > 0 ? 1.f / l : 0.f;
-      const float lse2 = w.T > 0 ? m + log2f(l) : -INFINITY;
-      const int64_t flat = (int64_t)w.bh * a.Lq + qrow;
-      if (w.T > 0) {
-        if (!__all_sync(0xffffffffu, mbar_wait(&o_full[x], outs & 1, abort))) {
-          ok = false;
-          break;
-        }
-        ++outs;
-        fence_after_sync();
-      }
-      if (a.splits > 1) {
-        const int64_t at = (int64_t)w.split * a.BH * a.Lq + flat;
-        if (in) a.part_lse[at] = lse2;
-        if (w.T == 0) continue;  // weight zero: the share's output is not read
-#pragma unroll 1
-        for (int ch = 0; ch < D / 32; ++ch) {
-          uint32_t o[32];
-          tmem_ld32(obase + ch * 32, o);
-          tmem_wait_ld();
-          if (in) {
-            float4* dst = reinterpret_cast<float4*>(a.part + at * D + ch * 32);
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              dst[e] = make_float4(__uint_as_float(o[4 * e]) * inv, __uint_as_float(o[4 * e + 1]) * inv,
-                                   __uint_as_float(o[4 * e + 2]) * inv, __uint_as_float(o[4 * e + 3]) * inv);
-          }
-        }
-      } else {
-        if (in && a.lse != nullptr) a.lse[flat] = lse2 * 0.6931471805599453f;
-#pragma unroll 1
-        for (int cb = 0; cb < CB; ++cb) {
-          uint32_t pk[32];
-#pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
-            uint32_t o[32];
-            tmem_ld32(obase + cb * 64 + hh * 32, o);  // without keys whatever is there: replaced
-            tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-              pk[hh * 16 + e] = w.T > 0 ? pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv)
-                                        : 0u;
-          }
-          if (lane == 0) tma_store_wait_read();  // what was in the buffer has left
-          __syncwarp();
-#pragma unroll
-          for (int c = 0; c < 8; ++c)
-            *reinterpret_cast<uint4*>(stage + lane * 128 + ((c ^ (lane & 7)) << 4)) =
-                make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
-          fence_async_shared();
-          __syncwarp();
-          if (lane == 0 && row0 < a.Lq) {
-            tma_store_4d(&tmO, stage, cb * 64, row0, w.h, w.b);
-            tma_store_commit();
-          }
-        }
-      }
-      fence_before_sync();  // before this tile's next P releases the P V that overwrites O
+      last = w;
+      last_m = m;
+      last_l = l;
+      open = true;
+    }
+    if (ok && open && __all_sync(0xffffffffu, mbar_wait(&pv_done[x], (steps - 1) & 1, abort))) {
+      fence_after_sync();
+      finish(last, last_m, last_l);
     }
     if (lane == 0) tma_store_wait();
   }

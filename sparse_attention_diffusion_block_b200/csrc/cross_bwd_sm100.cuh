@@ -333,15 +333,15 @@ cross_dq_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
     int steps = 0;
     bool ok = true;
     CrossItem w, nxt;
-    // -lse2 and -delta of this thread's row, read one item ahead; a row past
+    // lse and delta of this thread's row, read one item ahead; a row past
     // the end gives p = 0
-    float nl = -INFINITY, nd = 0.f;
+    float lse = INFINITY, delta = 0.f;
     auto row_values = [&](const CrossItem& v) {
       const int qrow = (v.tile + x) * 128 + row;
       const bool in = x < v.tiles && qrow < W.Lq;
       const int64_t flat = (int64_t)v.bh * W.Lq + qrow;
-      nl = in ? -a.lse[flat] * kLog2e : -INFINITY;
-      nd = in && v.nv > 64 ? -a.delta[flat] : 0.f;
+      lse = in ? a.lse[flat] : INFINITY;  // as read: arithmetic here would wait for them
+      delta = in && v.nv > 64 ? a.delta[flat] : 0.f;
     };
     int i = blockIdx.x;
     bool has = w.with_keys(W, i);
@@ -349,8 +349,9 @@ cross_dq_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
     while (ok && has) {
       i += gridDim.x;
       has = nxt.with_keys(W, i);
+      const float nl = -lse * kLog2e;
       const uint64_t nl2 = f2_pack(nl, nl);
-      float mine = nd;
+      float mine = -delta;
       if (has) row_values(nxt);
       const int T = x < w.tiles ? key_steps(w) : 0;
       for (int u = 0; u < T; ++u) {
@@ -466,7 +467,10 @@ cross_dq_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
 // columns of S^T and dP^T, so one's exponentials run under the other's MMAs; two
 // threads share a key row, 32 query columns each, which halves the time between
 // a step's scores and its P (with one thread a row: 1500 of 3400 cycles per two
-// steps, 0.61 ms for 32760 x 512, 40 heads).  Warp 16 loads, warp 17 issues.
+// steps, 0.61 against 0.58 ms for 32760 x 512, 40 heads).  Warp 16 loads, warp 17
+// issues.  (One S^T / dP^T buffer, handed on at once, with P^T and dS^T in columns
+// of their own and two issuers, as in the forward kernel: 0.62 ms; S^T and dP^T of
+// a step take 850 cycles here, and the hand-over of a single buffer shows.)
 // TMEM columns: [128x, +64) S^T, [128x + 64, +64) dP^T, [256, +D) dV, [256 + D, +D) dK.
 //
 // Work: the (batch, key head, key tile) items times the steps of all query
@@ -489,16 +493,19 @@ struct CrossDkvArgs {
   float scale_log2;
 };
 
-constexpr int kDkvStages = 4, kDkvThreads = 640;
+constexpr int kDkvThreads = 640;
 
 template <int D>
 struct CrossDkvLayout {
+  // Steps in shared memory: with four of d = 64 the loads' latency showed (24
+  // heads, 32760 x 512: 0.325 ms, with eight 0.292); four of d = 128 fill it.
+  static constexpr int kStages = D == 64 ? 8 : 4;
   static constexpr uint32_t kKeys = 128u * D * 2u;  // one of K, V
   static constexpr uint32_t kHalf = 64u * D * 2u;   // one of Q, G of a step
   static constexpr uint32_t kSlot = 2 * kHalf;
-  static constexpr int kNumBars = 2 * kDkvStages + 2 + 2 + 2 + 2 + 1 + 1;  // even: what follows is 16-byte aligned
+  static constexpr int kNumBars = 2 * kStages + 2 + 2 + 2 + 2 + 1 + 1;  // even: what follows is 16-byte aligned
   static constexpr size_t bytes() {
-    return 1024 + 2 * kKeys + kDkvStages * kSlot + kNumBars * 8 + 16 + 16 * 2 * 64 * sizeof(float);
+    return 1024 + 2 * kKeys + kStages * kSlot + kNumBars * 8 + 16 + 16 * 2 * 64 * sizeof(float);
   }
 };
 
@@ -580,7 +587,7 @@ cross_dkv_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
                        const __grid_constant__ CrossDkvArgs a) {
   using namespace sm100;
   using Lay = CrossDkvLayout<D>;
-  constexpr int CB = D / 64, NS = kDkvStages;
+  constexpr int CB = D / 64, NS = Lay::kStages;
   constexpr uint32_t KEYS = Lay::kKeys, HALF = Lay::kHalf, SLOT = Lay::kSlot, DV = 256, DK = 256 + D;
 
   extern __shared__ uint8_t smem_raw[];
@@ -735,14 +742,14 @@ cross_dkv_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
     const uint32_t sbase = lane_base + x * 128 + half * 32;  // this thread's scores; its P goes over their first half
     const uint64_t c2x2 = f2_pack(a.scale_log2, a.scale_log2);
     // Each warp keeps its own copy of its 32 columns' -lse2 and -delta (a row a
-    // lane, read one step ahead), so that no barrier but the bounded ones
+    // lane, read two steps ahead), so that no barrier but the bounded ones
     // stands between warps.  A row past the end gives p = 0.
     float* cv = colv + warp * 128;
     auto columns = [&](int u) -> float2 {
       const int q = u % ks.per_head * 64 + half * 32 + lane;
-      if (q >= a.Lq) return make_float2(-INFINITY, 0.f);
+      if (q >= a.Lq) return make_float2(INFINITY, 0.f);
       const int64_t at = ((int64_t)pc.b * a.heads + pc.hk * ks.group + u / ks.per_head) * a.Lq + q;
-      return make_float2(-a.lse[at] * kLog2e, -a.delta[at]);
+      return make_float2(a.lse[at], a.delta[at]);  // as read: arithmetic here would wait for them
     };
     int gs = 0, mine = 0, pieces = 0;
     bool ok = true;
@@ -752,8 +759,8 @@ cross_dkv_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       if (t < pc.n) cval = columns(pc.u0 + t);
       for (; t < pc.n; t += 2, ++mine) {
         float* cb = cv + (mine & 1) * 64;
-        cb[lane] = cval.x;
-        cb[32 + lane] = cval.y;
+        cb[lane] = -cval.x * kLog2e;
+        cb[32 + lane] = -cval.y;
         __syncwarp();
         if (t + 2 < pc.n) cval = columns(pc.u0 + t + 2);
         if (!__all_sync(0xffffffffu, mbar_wait(&s_full[x], mine & 1, abort))) {

@@ -535,12 +535,16 @@ struct CrossKeySpace {
       ranges = min((int64_t)ctas, (heads * steps + least - 1) / least);
     }
   }
-  __device__ __forceinline__ int64_t start(int64_t g) const { return g < ranges ? heads * steps * g / ranges : heads * steps; }
+  __device__ __forceinline__ int64_t start(int64_t g) const {
+    return g < ranges ? heads * steps * g / ranges : heads * steps;
+  }
   // the range that holds step x of a lane
   __device__ __forceinline__ int64_t owner(int64_t x) const { return ((x + 1) * ranges - 1) / (heads * steps); }
   // where the piece of range g in item `item` of lane j puts its sums: both only
   // grow along a lane, and one of them does from piece to piece
-  __device__ __forceinline__ int64_t slot(int64_t item, int64_t g, int j) const { return item + g + j * (heads + ranges); }
+  __device__ __forceinline__ int64_t slot(int64_t item, int64_t g, int j) const {
+    return item + g + j * (heads + ranges);
+  }
 };
 
 // A CTA's pieces in order: key tile j of (b, hk), steps [u0, u0 + n).
@@ -714,15 +718,15 @@ cross_dkv_sm100_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
         // the sums of the piece before have been read
         if (t == 0 && pieces > 0 && !(ok = mbar_wait(epi_done, (pieces - 1) & 1, abort))) break;
         fence_after_sync();
-        const uint32_t qb = ring + s * SLOT;
+        const uint32_t qb = ring + s * SLOT, pb = tmem + x * 128;  // P: 16 columns in each half of S^T's
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          mma_ts_warp(tmem + DV, tmem + x * 128 + (kk >> 1) * 32 + (kk & 1) * 8, desc_sw128(qb + HALF + kk * 16 * 128, 64 * 128, 1024), idO,
-                      (t > 0 || kk > 0) ? 1u : 0u);
+          mma_ts_warp(tmem + DV, pb + (kk >> 1) * 32 + (kk & 1) * 8, desc_sw128(qb + HALF + kk * 16 * 128, 64 * 128, 1024),
+                      idO, (t > 0 || kk > 0) ? 1u : 0u);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          mma_ts_warp(tmem + DK, tmem + x * 128 + 64 + (kk >> 1) * 32 + (kk & 1) * 8, desc_sw128(qb + kk * 16 * 128, 64 * 128, 1024), idO,
-                      (t > 0 || kk > 0) ? 1u : 0u);
+          mma_ts_warp(tmem + DK, pb + 64 + (kk >> 1) * 32 + (kk & 1) * 8, desc_sw128(qb + kk * 16 * 128, 64 * 128, 1024),
+                      idO, (t > 0 || kk > 0) ? 1u : 0u);
         mma_commit_warp(&empty[s]);
         if (t + 2 < pc.n) s_mmas(x);
       }

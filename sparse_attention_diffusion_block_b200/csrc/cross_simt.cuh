@@ -10,9 +10,10 @@
 // fp32 products stay on the CUDA cores: the fp32 tolerance leaves no room for
 // tf32 or bf16 operands.  Bound by the FMA pipe and by shared-memory reads once
 // the tiles fill the GPU.  Tiles come by cp.async while the threads work on the
-// ones before; the inner products are packed two to an instruction.  A key that is not allowed is read as a zero row (so whatever its memory
-// holds, NaN included, meets no product), and p and ds of its column are zero.
-// A row without any allowed key gives o = 0, lse = -inf and zero gradients.
+// ones before; the inner products are packed two to an instruction.
+// A key that is not allowed is read as a zero row (so whatever its memory holds,
+// NaN included, meets no product), and p and ds of its column are zero.  A row
+// without any allowed key gives o = 0, lse = -inf and zero gradients.
 #pragma once
 
 #include "common.cuh"

@@ -5,6 +5,7 @@
 #include "cross_simt.cuh"
 #include "fused_sm100.cuh"
 #include "sm100.cuh"
+#include "tma4.cuh"
 
 namespace pisa {
 

@@ -102,6 +102,30 @@ def test_masks_with_holes_and_garbage_behind_them(lib, Lq, with_len, dtype):
 
 
 @DTYPES
+@pytest.mark.parametrize("Lq", [1, 300])
+def test_no_keys_at_all(lib, Lq, dtype):
+    q, k, v, g = _make(19, 2, 4, 2, Lq, 200, 128, dtype)
+    lens = torch.zeros(2, dtype=torch.int32, device="cuda")
+    out, lse = lib.cross_attn_fwd(q, k, v, kv_len=lens, return_lse=True)
+    assert (out == 0).all() and (lse == -float("inf")).all()
+    for y in lib.cross_attn_bwd(g, q, k, v, out, lse, kv_len=lens):
+        assert (y == 0).all()
+    assert lib.device_status() == 0
+
+
+@DTYPES
+@pytest.mark.parametrize("Lq,Lk", [(1, 1), (1, 40), (40, 1)])
+def test_strided_rows_of_length_one(lib, Lq, Lk, dtype):
+    """Views whose single row has the stride of a longer buffer."""
+    q = _x(33, 2, 5, 3, 64, dtype=dtype)[:, :Lq].permute(0, 2, 1, 3) if Lq == 1 else \
+        _x(33, 2, Lq, 3, 64, dtype=dtype).permute(0, 2, 1, 3)
+    kv = _x(34, 2, Lk + 3, 2, 3, 64, dtype=dtype)[:, 1:1 + Lk]
+    k, v = (kv[:, :, i].permute(0, 2, 1, 3) for i in (0, 1))
+    g = _x(35, 2, 3, Lq, 64, dtype=dtype)
+    _check(lib, q, k, v, g, what="one row")
+
+
+@DTYPES
 def test_large_scores(lib, dtype):
     """Scores far apart: the running maximum moves late, most keys underflow."""
     q, k, v, g = _make(6, 1, 2, 2, 140, 400, 64, dtype)

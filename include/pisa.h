@@ -403,8 +403,9 @@ pisa_status pisa_rope(const void* q, void* q_out, const void* k, void* k_out, pi
  * dv} (backward), or NULL when all are dense.  Every stride of a dimension
  * larger than 1 is a multiple of 16 bytes and at least d (so no broadcast
  * tensors); pointers are 16-byte aligned, kv_len and lse 4-byte, key_mask any.
- * d in {64, 128}, batch * heads <= 65535.  Softmax statistics and sums are
- * 32-bit; with bf16 inputs p and ds enter their products rounded to bf16. */
+ * d in {64, 128}, batch * heads <= 65535.  Outputs and workspace overlap nothing
+ * else, and a workspace serves one call at a time.  Softmax statistics and sums
+ * are 32-bit; with bf16 inputs p and ds enter their products rounded to bf16. */
 
 /* Scratch bytes of pisa_cross_attn_fwd (backward = 0) or pisa_cross_attn_bwd
  * (backward = 1); masked: whether kv_len or key_mask is given.  0 for an

@@ -542,6 +542,8 @@ def _cross_workspace(need: int, device, given: Optional[torch.Tensor]):
         if need <= 16:
             return None, None, 0
         given = torch.empty(need, dtype=torch.uint8, device=device)
+    elif given.device != device or not given.is_contiguous():
+        raise ValueError("workspace must be contiguous, on the tensors' device")
     return given, given.data_ptr(), given.numel() * given.element_size()
 
 

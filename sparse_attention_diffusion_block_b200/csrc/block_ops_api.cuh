@@ -189,7 +189,6 @@ CrossPackPlan cross_pack_plan(const CrossShape& s, bool backward) {
   return p;
 }
 
-// Few query rows per key head go through cross_rows_kernel.
 // Few query rows per key head go through cross_rows_kernel: with bf16 one (80
 // heads of 4608 x 128 keys: 44 us, the tensor-core kernel takes 66 for any
 // number up to 128; with two rows and 24 heads of 512 keys it is ahead, 9.8 to

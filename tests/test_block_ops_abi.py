@@ -152,3 +152,14 @@ def test_binding_refuses_tensors(lib):
         lib.cross_attn_fwd(t, t, t)  # host tensors
     with pytest.raises(ValueError):
         lib.rope(t, t, torch.zeros(8, 1), (64,))
+
+
+def test_binding_refuses_workspaces(lib):
+    """A workspace's bytes are one run of the tensors' own device's memory."""
+    host, cuda = torch.device("cpu"), torch.device("cuda", 0)
+    ok = torch.zeros(64, dtype=torch.uint8)
+    assert lib._cross_workspace(64, host, ok)[1:] == (ok.data_ptr(), 64)
+    for bad, device in ((ok, cuda), (torch.zeros(1, dtype=torch.uint8).expand(1 << 20), host),
+                        (torch.zeros(128, dtype=torch.uint8)[::2], host)):
+        with pytest.raises(ValueError):
+            lib._cross_workspace(64, device, bad)
